@@ -6,7 +6,7 @@ Three operators stand next to the head's own entry points:
   logits, with the greedy choice of every row, before a token is drawn or a drafted block verified;
 * ``block_cross_entropy``: the teacher-forced training loss on corrected logits together with its
   gradient, which ``apply_block_logits_backward`` takes;
-* ``clip_grad_norm``: the global norm over the head's (and any other) gradients, and clipping by it.
+* ``GradientClipper``: the global norm over the head's (and any other) gradients, and clipping by it.
 """
 import math
 
@@ -184,6 +184,10 @@ def _prepare_clip(case, gen):
         s[name] = views
     elements = sum(n for _, n in sizes[1:])
     s["max_norm"] = 1e-3 * math.sqrt(elements) * (0.31 if case["clip"] else 3.1)
+    if own:
+        # A training program's gradient buffers stay where they are, and so does the object that knows them.
+        from rank_markov_draft_vanillamarkov_b200 import GradientClipper
+        s["clipper"] = GradientClipper(s["grads"], out=s["outs"])
     return s
 
 
@@ -266,8 +270,7 @@ def run(s):
         loss, rows, grad = head.block_cross_entropy(s["logits"], s["targets"], weights=s["weights"],
                                                     ignore_index=IGNORE, reduction="mean", out_grad=s["grad"])
         return {"loss": loss, "rows": rows, "grad": grad}
-    norm = head.clip_grad_norm(s["grads"], s["max_norm"], out=s["outs"])
-    return {"norm": norm, "grads": s["out"]}
+    return {"norm": s["clipper"].clip(s["max_norm"]), "grads": s["out"]}
 
 
 # -------------------------------------------------------- work and 64 bits --
