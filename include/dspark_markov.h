@@ -230,6 +230,178 @@ int dspark_markov_sample_block_noalloc(const void* base_logits, const int64_t* f
                                        void* stream);
 
 /*
+ * Token constraints on corrected logits, with the choice of every row: the
+ * step between the head's corrected logits and the token, for one position of
+ * each sequence (block 1) or for a whole block of them (a drafted block that a
+ * verifier looks at). For row (b, k) let n_v be the occurrences of id v among
+ * sequence b's generated tokens (its history past the prompt) and the drafted
+ * tokens before position k, and let s_v hold where n_v > 0 or v is in the
+ * prompt. Each logit x goes through, in fp32 and in this order,
+ *
+ *     s_v:              x = x > 0 ? x / repetition : x * repetition
+ *     n_v > 0:          x = (x - frequency * n_v) - presence
+ *     a bias names v:   x = x + bias
+ *     v not allowed:    x = -inf
+ *
+ * and is rounded once (nearest even) to the logits dtype. Without a clause's
+ * inputs the clause does nothing; an infinity or a NaN in an allowed place goes
+ * through the same arithmetic. A row whose mask leaves nothing is all -inf.
+ */
+typedef struct dspark_markov_constraints {
+  /* [batch, history_stride] int64, the first history_lens[b] (at most
+   * history_cap) ids of row b are sequence b's tokens and the first
+   * prompt_lens[b] of those its prompt. history NULL: none; history_lens NULL:
+   * history_cap everywhere; prompt_lens NULL: 0 everywhere. Lengths are
+   * clamped to their range. */
+  const int64_t* history;
+  int64_t history_cap, history_stride;
+  const int64_t* history_lens;
+  const int64_t* prompt_lens;
+  /* [batch] fp32 each, or NULL for the one value beside it. Values that change
+   * nothing: 1, 0, 0. */
+  const float* repetition;
+  const float* frequency;
+  const float* presence;
+  float repetition_value, frequency_value, presence_value;
+  /* bias_count pairs for each sequence, rows bias_stride apart (0: the same
+   * pairs for all). A negative id is an unused entry; of several entries with
+   * one id the last counts. */
+  int64_t bias_count, bias_stride;
+  const int64_t* bias_ids;
+  const float* bias_values;
+} dspark_markov_constraints;
+
+/*
+ *   logits, out     [batch, block, vocab] logits_dtype with unit stride along
+ *                   vocab and the given strides (elements) between sequences
+ *                   and between rows. out may equal logits with equal strides;
+ *                   other overlaps are DSPARK_ERR_INVALID_ARG.
+ *   constraints     host struct of device pointers, read during the call.
+ *   draft_tokens    [batch, draft_stride] int64 or NULL: row (b, k) follows the
+ *                   first draft_first + k entries of row b. A negative entry
+ *                   is padding and counts for nothing.
+ *   allowed         words of 32 bits, bit v % 32 of word v / 32 of a row set
+ *                   where v is allowed, or NULL (all allowed); rows at the
+ *                   given strides in words (0 where a row serves several).
+ *   tokens          [batch, tokens_stride] int64 or NULL: the choice of row
+ *                   (b, k) at b * tokens_stride + k, made on the rounded
+ *                   values like dspark_markov_sample_block's (temperature
+ *                   below 1e-5: the lowest index of the largest; otherwise a
+ *                   Gumbel-max draw at step draft_first + k of the seed).
+ *   scratch         dspark_markov_constrain_scratch_bytes() bytes of device
+ *                   memory, 8-byte aligned, needed where tokens is not NULL.
+ *                   It may be reused once the call's work has run; calls that
+ *                   overlap take one each.
+ *
+ * An id at or above vocab (or a negative one inside a history) is left out and
+ * sets DSPARK_STATUS_TOKEN_RANGE. batch == 0 or block == 0 is OK and enqueues
+ * nothing.
+ */
+int dspark_markov_process_logits(const void* logits, void* out, int64_t batch, int64_t block, int64_t vocab,
+                                 int64_t in_batch_stride, int64_t in_row_stride, int64_t out_batch_stride,
+                                 int64_t out_row_stride, const dspark_markov_constraints* constraints,
+                                 const int64_t* draft_tokens, int64_t draft_stride, int64_t draft_first,
+                                 const void* allowed, int64_t allowed_batch_stride, int64_t allowed_row_stride,
+                                 int64_t* tokens, int64_t tokens_stride, float temperature, uint64_t seed,
+                                 void* scratch, int32_t logits_dtype, void* stream);
+
+/* Scratch bytes of the calls that choose tokens under constraints; 0 for sizes they refuse. */
+int64_t dspark_markov_constrain_scratch_bytes(int64_t batch, int64_t block, int64_t vocab);
+
+/*
+ * dspark_markov_sample_block under token constraints: position k's corrected
+ * logits go through dspark_markov_process_logits with the block's own earlier
+ * tokens as the drafted ones before the choice, and corrected_logits receives
+ * the processed values. One correction and one constraint step per position
+ * (the tensor-core or the generic kernels as for
+ * dspark_markov_apply_block_logits), so constraints cost launches that the
+ * unconstrained sampler does not have. `allowed` rows are those of the block's
+ * positions; scratch as for (batch, 1, vocab), so that calls that overlap take
+ * one each. Other arguments, ownership and errors as for
+ * dspark_markov_sample_block.
+ */
+int dspark_markov_sample_block_constrained(const void* base_logits, const int64_t* first_prev_token_ids,
+                                           int64_t batch, int64_t proposal_len, int64_t vocab, const void* w1,
+                                           const void* w2, int32_t rank, float temperature, uint64_t seed,
+                                           const dspark_markov_constraints* constraints, const void* allowed,
+                                           int64_t allowed_batch_stride, int64_t allowed_row_stride,
+                                           int64_t* sampled_tokens, void* corrected_logits, void* scratch,
+                                           int32_t logits_dtype, int32_t weight_dtype, void* stream);
+
+/*
+ * The teacher-forced training loss on corrected logits with its gradient, the
+ * grad_out of dspark_markov_apply_block_logits_backward. Row i is live when
+ * targets[i] is not ignore_index and its weight is not zero; with lse_i =
+ * log sum_v exp(c_iv) over the row's logits c_i and N = sum of the live rows'
+ * weights (mean) or 1,
+ *
+ *     row_losses[i] = lse_i - c_i[t_i]                      (0 in other rows)
+ *     loss          = sum_i w_i row_losses[i] / N           (0 where N is 0)
+ *     grad[i, v]    = w_i / N (exp(c_iv - lse_i) - [v = t_i])   (0 in other rows)
+ *
+ *   logits      [rows, vocab] logits_dtype. Rows that are not live are not read.
+ *   targets     [rows] int64; an id outside [0, vocab) that is not ignore_index
+ *               makes its row not live and sets DSPARK_STATUS_TOKEN_RANGE.
+ *   weights     [rows] fp32, or NULL: all 1.
+ *   loss        one fp32 element, row_losses [rows] fp32, both written.
+ *   grad        [rows, vocab] logits_dtype, written, or NULL (not wanted); may
+ *               equal logits, other overlaps are DSPARK_ERR_INVALID_ARG.
+ *   scratch     DSPARK_LOSS_SCRATCH_BYTES bytes of device memory, 8-byte
+ *               aligned; calls that overlap take one each.
+ *
+ * Sums are fp32 or wider and in a fixed order; the gradient is rounded once. A
+ * live row that holds NaN or +inf, or -inf everywhere, has a NaN loss and
+ * gradient. rows == 0 writes loss = 0.
+ */
+#define DSPARK_LOSS_SCRATCH_BYTES 64
+int dspark_markov_block_cross_entropy(const void* logits, const int64_t* targets, const float* weights, int64_t rows,
+                                      int64_t vocab, int64_t ignore_index, int32_t mean, float* loss,
+                                      float* row_losses, void* grad, void* scratch, int32_t logits_dtype,
+                                      void* stream);
+
+/*
+ * The global norm over many gradient tensors and clipping by it:
+ *
+ *     norm = sqrt(sum over all elements of g^2)
+ *     out  = g * min(1, max_norm / (norm + 1e-6))
+ *
+ * A plan lists the tensors cut into pieces. dspark_markov_clip_plan fills it on
+ * the host from the tensors' addresses, sizes and dtypes; the caller copies it
+ * to device memory and keeps it with the tensors for as many calls as it likes.
+ */
+typedef struct dspark_markov_clip_piece {
+  const void* grad;
+  void* out; /* equal to grad: in place */
+  int32_t count;
+  int32_t dtype;
+} dspark_markov_clip_piece;
+
+/*
+ * Writes the plan of `tensors` tensors (host arrays; counts in elements, zero
+ * allowed) to `plan`, which holds `capacity` pieces, and their number to
+ * *pieces. With plan == NULL only counts. A tensor's out equals its grad or
+ * overlaps no tensor's grad or out; tensors do not overlap one another
+ * (checked; DSPARK_ERR_INVALID_ARG). Addresses are multiples of the element
+ * size. No device call is made.
+ */
+int dspark_markov_clip_plan(const void* const* grads, void* const* outs, const int64_t* counts,
+                            const int32_t* dtypes, int64_t tensors, dspark_markov_clip_piece* plan, int64_t capacity,
+                            int64_t* pieces);
+
+/*
+ * Runs a plan (device memory). norm: one fp32 element, written. scratch:
+ * DSPARK_CLIP_SCRATCH_BYTES bytes of device memory, 8-byte aligned; calls that
+ * overlap take one each. The sum of squares is formed in 64 bits from groups of
+ * a few 32-bit sums, in an order fixed by the plan, and holds for any finite
+ * values. An infinite norm scales by 0 and a NaN norm by NaN, as the formula
+ * says; max_norm is not negative and not NaN. pieces == 0 writes norm = 0.
+ */
+#define DSPARK_CLIP_MAX_PARTIALS 1024
+#define DSPARK_CLIP_SCRATCH_BYTES 8192
+int dspark_markov_clip_grad_norm(const dspark_markov_clip_piece* plan, int64_t pieces, float max_norm, float* norm,
+                                 void* scratch, void* stream);
+
+/*
  * Synchronise `stream`, then read and clear the current device's status word
  * (DSPARK_STATUS_* bits) into *status_out. Not part of the hot path.
  */

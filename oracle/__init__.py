@@ -29,3 +29,4 @@ from .philox import gumbel_noise, noise_words, philox4x32, uniform_from_word  # 
 from .rounding import round_to, round_to_bfloat16, round_to_float32, ulp_bfloat16  # noqa: F401
 from .checks import (accumulation_bound, check_logits, check_sampled_block, check_tokens,  # noqa: F401
                      fused_accumulation_bound)
+from . import around  # noqa: F401,E402

@@ -7,7 +7,10 @@ loudly if it has not been built.
 """
 from .head import (VanillaMarkov, build_markov_head, device_status, last_algo, last_variant, launch_count,  # noqa: F401
                    set_algo, set_debug)
+from .constraints import TokenConstraints, process_logits  # noqa: F401
+from .training import GradientClipper, block_cross_entropy, clip_grad_norm  # noqa: F401
 from ._native import DSparkError  # noqa: F401
 
 __all__ = ["VanillaMarkov", "build_markov_head", "device_status", "set_algo", "launch_count", "last_algo",
-           "last_variant", "set_debug", "DSparkError"]
+           "last_variant", "set_debug", "DSparkError", "TokenConstraints", "process_logits", "block_cross_entropy",
+           "GradientClipper", "clip_grad_norm"]

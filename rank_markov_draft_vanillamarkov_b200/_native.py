@@ -38,6 +38,27 @@ DSPARK_VARIANT_BWD_RESIDENT_W1 = 1
 DSPARK_VARIANT_SAMPLE_ROWS = 2
 DSPARK_VARIANT_APPLY_WIDE = 4
 
+DSPARK_LOSS_SCRATCH_BYTES = 64
+DSPARK_CLIP_MAX_PARTIALS = 1024
+DSPARK_CLIP_SCRATCH_BYTES = 8192
+
+
+class Constraints(ctypes.Structure):
+    """dspark_markov_constraints."""
+    _fields_ = [("history", ctypes.c_void_p), ("history_cap", ctypes.c_int64), ("history_stride", ctypes.c_int64),
+                ("history_lens", ctypes.c_void_p), ("prompt_lens", ctypes.c_void_p), ("repetition", ctypes.c_void_p),
+                ("frequency", ctypes.c_void_p), ("presence", ctypes.c_void_p),
+                ("repetition_value", ctypes.c_float), ("frequency_value", ctypes.c_float),
+                ("presence_value", ctypes.c_float), ("bias_count", ctypes.c_int64), ("bias_stride", ctypes.c_int64),
+                ("bias_ids", ctypes.c_void_p), ("bias_values", ctypes.c_void_p)]
+
+
+class ClipPiece(ctypes.Structure):
+    """dspark_markov_clip_piece."""
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("count", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
 # Every symbol include/dspark_markov.h declares, with its ctypes signature.
 _vp, _i64, _i32, _u32, _u64, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_float
 SIGNATURES = {
@@ -51,6 +72,15 @@ SIGNATURES = {
                                                           _i32, _i32, _vp]),
     "dspark_markov_sample_block_noalloc": (ctypes.c_int, [_vp, _vp, _i64, _i64, _i64, _vp, _vp, _i32, _f32, _u64,
                                                           _vp, _vp, _i32, _i32, _vp]),
+    "dspark_markov_process_logits": (ctypes.c_int, [_vp, _vp, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _i64,
+                                                    _i64, _vp, _i64, _i64, _vp, _i64, _f32, _u64, _vp, _i32, _vp]),
+    "dspark_markov_constrain_scratch_bytes": (_i64, [_i64, _i64, _i64]),
+    "dspark_markov_sample_block_constrained": (ctypes.c_int, [_vp, _vp, _i64, _i64, _i64, _vp, _vp, _i32, _f32, _u64,
+                                                              _vp, _vp, _i64, _i64, _vp, _vp, _vp, _i32, _i32, _vp]),
+    "dspark_markov_block_cross_entropy": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp,
+                                                         _i32, _vp]),
+    "dspark_markov_clip_plan": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _vp, _i64, ctypes.POINTER(_i64)]),
+    "dspark_markov_clip_grad_norm": (ctypes.c_int, [_vp, _i64, _f32, _vp, _vp, _vp]),
     "dspark_markov_get_status": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_int32)]),
     "dspark_markov_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "dspark_markov_set_algo": (_i32, [_i32]),

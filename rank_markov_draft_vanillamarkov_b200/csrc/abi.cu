@@ -5,11 +5,15 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <new>
+#include <stdexcept>
+#include <vector>
 
 #include "../../include/dspark_markov.h"
 #include "kernels.h"
@@ -150,6 +154,64 @@ unsigned char* noalloc_scratch_if_ready() {
 }
 
 bool dtype_ok(int32_t t) { return t == DSPARK_DTYPE_FP32 || t == DSPARK_DTYPE_BF16; }
+
+// The binding lays these out by hand.
+static_assert(sizeof(dspark_markov_constraints) == 112 && sizeof(dspark_markov_clip_piece) == 24, "struct layout");
+
+bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// a * b + c for non-negative sizes, or -1 where it passes `limit`.
+int64_t bounded(int64_t a, int64_t b, int64_t c, int64_t limit) {
+  if (a < 0 || b < 0 || c < 0 || c > limit) return -1;
+  if (b != 0 && a > (limit - c) / b) return -1;
+  return a * b + c;
+}
+
+// Elements from the first to past the last of a [batch, block, vocab] layout,
+// or -1 where a stride is negative or the extent does not fit.
+int64_t extent(int64_t batch, int64_t block, int64_t vocab, int64_t batch_stride, int64_t row_stride) {
+  constexpr int64_t kMost = 1ll << 60;
+  if (batch_stride < 0 || row_stride < 0) return -1;
+  const int64_t rows = bounded(block - 1, row_stride, vocab, kMost);
+  return rows < 0 ? -1 : bounded(batch - 1, batch_stride, rows, kMost);
+}
+
+// Whether the rows of such a layout are disjoint (sequences outside rows, or
+// rows outside sequences).
+bool disjoint_rows(int64_t batch, int64_t block, int64_t vocab, int64_t batch_stride, int64_t row_stride) {
+  if (batch == 1) return block == 1 || row_stride >= vocab;
+  if (block == 1) return batch_stride >= vocab;
+  if (row_stride >= vocab && batch_stride >= extent(1, block, vocab, 0, row_stride)) return true;
+  return batch_stride >= vocab && row_stride >= extent(batch, 1, vocab, batch_stride, 0);
+}
+
+// The checks of a constraint struct that a call reads through.
+bool constraints_ok(const dspark_markov_constraints* c) {
+  if (!c || c->history_cap < 0 || c->history_stride < 0 || c->bias_count < 0 || c->bias_stride < 0) return false;
+  if (c->bias_count > 0 && (!c->bias_ids || !c->bias_values)) return false;
+  if (c->bias_count > 0x7fffffffll) return false;
+  return true;
+}
+
+ConstrainArgs constrain_args(const dspark_markov_constraints& c) {
+  ConstrainArgs a{};
+  a.history = c.history_cap > 0 ? c.history : nullptr;
+  a.history_cap = c.history_cap;
+  a.history_stride = c.history_stride;
+  a.history_lens = c.history_lens;
+  a.prompt_lens = c.prompt_lens;
+  a.repetition = c.repetition;
+  a.frequency = c.frequency;
+  a.presence = c.presence;
+  a.repetition_value = c.repetition_value;
+  a.frequency_value = c.frequency_value;
+  a.presence_value = c.presence_value;
+  a.bias_ids = c.bias_ids;
+  a.bias_values = c.bias_values;
+  a.bias_count = c.bias_count;
+  a.bias_stride = c.bias_stride;
+  return a;
+}
 
 int cuda_code(cudaError_t e) { return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA; }
 
@@ -475,6 +537,233 @@ int dspark_markov_sample_block_noalloc(const void* base_logits, const int64_t* f
   const cudaError_t e = launch_tc_sample(a, st->num_sms, s, sample_layout(), &variant);
   t_last_variant = variant;
   return cuda_code(e);
+}
+
+int64_t dspark_markov_constrain_scratch_bytes(int64_t batch, int64_t block, int64_t vocab) {
+  if (batch <= 0 || block <= 0 || vocab <= 0 || vocab > 0xfffffffell) return 0;
+  if (bounded(batch, block, 0, 0x7fffffffll) < 0) return 0;
+  return constrain_key_count(batch, block, vocab) * (int64_t)sizeof(unsigned long long);
+}
+
+int dspark_markov_process_logits(const void* logits, void* out, int64_t batch, int64_t block, int64_t vocab,
+                                 int64_t in_batch_stride, int64_t in_row_stride, int64_t out_batch_stride,
+                                 int64_t out_row_stride, const dspark_markov_constraints* constraints,
+                                 const int64_t* draft_tokens, int64_t draft_stride, int64_t draft_first,
+                                 const void* allowed, int64_t allowed_batch_stride, int64_t allowed_row_stride,
+                                 int64_t* tokens, int64_t tokens_stride, float temperature, uint64_t seed,
+                                 void* scratch, int32_t logits_dtype, void* stream) {
+  t_last_algo = 0;
+  t_last_variant = 0;
+  if (batch < 0 || block < 0 || vocab <= 0 || !dtype_ok(logits_dtype) || std::isnan(temperature) ||
+      !constraints_ok(constraints) || draft_first < 0 || draft_stride < 0 || allowed_batch_stride < 0 ||
+      allowed_row_stride < 0 || tokens_stride < 0)
+    return DSPARK_ERR_INVALID_ARG;
+  if (batch == 0 || block == 0) return DSPARK_OK;
+  if (!logits || !out || (tokens && !scratch)) return DSPARK_ERR_INVALID_ARG;
+  if (vocab > 0xfffffffell || bounded(batch, block, 0, 0x7fffffffll) < 0 || draft_first > 0x7fffffffll - block)
+    return DSPARK_ERR_UNSUPPORTED;
+  const size_t lsize = logits_dtype == DSPARK_DTYPE_BF16 ? 2 : 4;
+  const int64_t n_in = extent(batch, block, vocab, in_batch_stride, in_row_stride);
+  const int64_t n_out = extent(batch, block, vocab, out_batch_stride, out_row_stride);
+  if (n_in < 0 || n_out < 0 || !disjoint_rows(batch, block, vocab, out_batch_stride, out_row_stride) ||
+      !aligned_to(logits, lsize) || !aligned_to(out, lsize) || !aligned_to(scratch, 8))
+    return DSPARK_ERR_INVALID_ARG;
+  if (tokens && batch > 1 && tokens_stride < block) return DSPARK_ERR_INVALID_ARG;
+  if (draft_tokens && batch > 1 && draft_stride < draft_first + block - 1) return DSPARK_ERR_INVALID_ARG;
+  if (logits == out) {
+    if ((batch > 1 && in_batch_stride != out_batch_stride) || (block > 1 && in_row_stride != out_row_stride))
+      return DSPARK_ERR_INVALID_ARG;
+  } else {
+    const uintptr_t i0 = reinterpret_cast<uintptr_t>(logits), o0 = reinterpret_cast<uintptr_t>(out);
+    if (i0 < o0 + (uintptr_t)n_out * lsize && o0 < i0 + (uintptr_t)n_in * lsize) return DSPARK_ERR_INVALID_ARG;
+  }
+  int err = DSPARK_OK;
+  DeviceState* d = device_state(&err);
+  if (!d) return err;
+  ConstrainArgs a = constrain_args(*constraints);
+  a.in = logits;
+  a.out = out;
+  a.batch = batch;
+  a.block = block;
+  a.vocab = vocab;
+  a.in_batch = in_batch_stride;
+  a.in_row = in_row_stride;
+  a.out_batch = out_batch_stride;
+  a.out_row = out_row_stride;
+  a.draft = draft_tokens;
+  a.draft_stride = draft_stride;
+  a.draft_first = draft_first;
+  a.allowed = static_cast<const uint32_t*>(allowed);
+  a.allowed_batch = allowed_batch_stride;
+  a.allowed_row = allowed_row_stride;
+  a.keys = tokens ? static_cast<unsigned long long*>(scratch) : nullptr;
+  a.tokens = tokens;
+  a.tokens_batch = tokens_stride;
+  a.greedy = !(temperature >= 1e-5f) ? 1 : 0;
+  a.temperature = temperature;
+  a.seed = seed;
+  a.status = d->status;
+  t_last_algo = 1;
+  return cuda_code(launch_constrain(a, logits_dtype, d->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+int dspark_markov_sample_block_constrained(const void* base_logits, const int64_t* first_prev_token_ids,
+                                           int64_t batch, int64_t proposal_len, int64_t vocab, const void* w1,
+                                           const void* w2, int32_t rank, float temperature, uint64_t seed,
+                                           const dspark_markov_constraints* constraints, const void* allowed,
+                                           int64_t allowed_batch_stride, int64_t allowed_row_stride,
+                                           int64_t* sampled_tokens, void* corrected_logits, void* scratch,
+                                           int32_t logits_dtype, int32_t weight_dtype, void* stream) {
+  t_last_algo = 0;
+  t_last_variant = 0;
+  if (batch < 0 || proposal_len < 0 || vocab <= 0 || rank <= 0 || !dtype_ok(logits_dtype) ||
+      !dtype_ok(weight_dtype) || std::isnan(temperature) || !constraints_ok(constraints) ||
+      allowed_batch_stride < 0 || allowed_row_stride < 0)
+    return DSPARK_ERR_INVALID_ARG;
+  if (batch == 0 || proposal_len == 0) return DSPARK_OK;
+  if (!base_logits || !first_prev_token_ids || !w1 || !w2 || !sampled_tokens || !corrected_logits || !scratch ||
+      !aligned_to(scratch, 8))
+    return DSPARK_ERR_INVALID_ARG;
+  if (vocab > 0xfffffffell || bounded(batch, proposal_len, 0, 0x7fffffffll) < 0) return DSPARK_ERR_UNSUPPORTED;
+  const size_t lsize = logits_dtype == DSPARK_DTYPE_BF16 ? 2 : 4;
+  const int64_t n = extent(batch, proposal_len, vocab, proposal_len * vocab, vocab);
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(base_logits), c0 = reinterpret_cast<uintptr_t>(corrected_logits);
+  if (n < 0 || !aligned_to(base_logits, lsize) || !aligned_to(corrected_logits, lsize)) return DSPARK_ERR_INVALID_ARG;
+  // The corrected logits are written while base logits are still being read.
+  if (a0 < c0 + (uintptr_t)n * lsize && c0 < a0 + (uintptr_t)n * lsize) return DSPARK_ERR_INVALID_ARG;
+  int err = DSPARK_OK;
+  DeviceState* d = device_state(&err);
+  if (!d) return err;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int32_t algo = g_algo.load();
+  const bool tc_ok = tc_apply_supported(batch, vocab, rank, logits_dtype, weight_dtype) &&
+                     aligned_to(base_logits, 16) && aligned_to(corrected_logits, 16) && aligned_to(w1, 16) &&
+                     aligned_to(w2, 16);
+  if (algo == DSPARK_ALGO_TENSOR_CORE && !tc_ok) return DSPARK_ERR_UNSUPPORTED;
+  const bool tc = tc_ok && algo != DSPARK_ALGO_GENERIC;
+  t_last_algo = tc ? 2 : 1;
+  ConstrainArgs c = constrain_args(*constraints);
+  c.batch = batch;
+  c.block = 1;
+  c.vocab = vocab;
+  c.in_batch = c.out_batch = proposal_len * vocab;
+  c.draft = sampled_tokens;
+  c.draft_stride = proposal_len;
+  c.allowed_batch = allowed_batch_stride;
+  c.keys = static_cast<unsigned long long*>(scratch);
+  c.tokens_batch = proposal_len;
+  c.greedy = !(temperature >= 1e-5f) ? 1 : 0;
+  c.temperature = temperature;
+  c.seed = seed;
+  c.status = d->status;
+  for (int64_t k = 0; k < proposal_len; ++k) {
+    const void* in = static_cast<const char*>(base_logits) + (size_t)k * vocab * lsize;
+    void* out = static_cast<char*>(corrected_logits) + (size_t)k * vocab * lsize;
+    const int64_t* prev = k == 0 ? first_prev_token_ids : sampled_tokens + (k - 1);
+    const int64_t ld = proposal_len * vocab, ld_id = k == 0 ? 1 : proposal_len;
+    cudaError_t e;
+    if (tc) {
+      TcApplyArgs a{in, out, prev, batch, vocab, w1, w2, rank, d->status, g_wait_limit_ns.load(),
+                    logits_dtype == DSPARK_DTYPE_FP32 ? 1 : 0, ld, ld, ld_id};
+      e = launch_tc_apply(a, d->num_sms, s);
+    } else {
+      GenericApplyArgs a{in, out, prev, batch, vocab, ld, ld, ld_id, w1, w2, rank, d->status};
+      e = launch_generic_apply(a, logits_dtype, weight_dtype, s);
+    }
+    if (e != cudaSuccess) return DSPARK_ERR_CUDA;
+    c.in = out;
+    c.out = out;
+    c.draft_first = k;
+    c.allowed = allowed ? static_cast<const uint32_t*>(allowed) + k * allowed_row_stride : nullptr;
+    c.tokens = sampled_tokens + k;
+    e = launch_constrain(c, logits_dtype, d->num_sms, s);
+    if (e != cudaSuccess) return DSPARK_ERR_CUDA;
+  }
+  return DSPARK_OK;
+}
+
+int dspark_markov_block_cross_entropy(const void* logits, const int64_t* targets, const float* weights, int64_t rows,
+                                      int64_t vocab, int64_t ignore_index, int32_t mean, float* loss,
+                                      float* row_losses, void* grad, void* scratch, int32_t logits_dtype,
+                                      void* stream) {
+  t_last_algo = 0;
+  t_last_variant = 0;
+  if (rows < 0 || vocab <= 0 || !dtype_ok(logits_dtype) || !loss || !scratch || !aligned_to(scratch, 8))
+    return DSPARK_ERR_INVALID_ARG;
+  if (rows > 0 && (!logits || !targets || !row_losses)) return DSPARK_ERR_INVALID_ARG;
+  const size_t lsize = logits_dtype == DSPARK_DTYPE_BF16 ? 2 : 4;
+  if (!aligned_to(logits, lsize) || !aligned_to(grad, lsize)) return DSPARK_ERR_INVALID_ARG;
+  if (rows > 0x7fffffffll || bounded(rows, vocab, 0, 1ll << 60) < 0) return DSPARK_ERR_UNSUPPORTED;
+  if (grad && grad != logits) {
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(logits), g0 = reinterpret_cast<uintptr_t>(grad);
+    const uintptr_t n = (uintptr_t)(rows * vocab) * lsize;
+    if (a0 < g0 + n && g0 < a0 + n) return DSPARK_ERR_INVALID_ARG;
+  }
+  int err = DSPARK_OK;
+  DeviceState* d = device_state(&err);
+  if (!d) return err;
+  LossArgs a{logits, targets, weights, rows, vocab, ignore_index, mean ? 1 : 0, loss, row_losses, grad, scratch,
+             d->status};
+  t_last_algo = 1;
+  return cuda_code(launch_loss(a, logits_dtype, d->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+int dspark_markov_clip_plan(const void* const* grads, void* const* outs, const int64_t* counts,
+                            const int32_t* dtypes, int64_t tensors, dspark_markov_clip_piece* plan, int64_t capacity,
+                            int64_t* pieces) {
+  if (tensors < 0 || capacity < 0 || !pieces || (tensors > 0 && (!grads || !outs || !counts || !dtypes)))
+    return DSPARK_ERR_INVALID_ARG;
+  struct Range {
+    uintptr_t lo, hi;
+  };
+  try {
+    std::vector<Range> ranges;
+    ranges.reserve((size_t)tensors * 2);
+    int64_t n = 0;
+    for (int64_t i = 0; i < tensors; ++i) {
+      if (!dtype_ok(dtypes[i]) || counts[i] < 0 || counts[i] > 1ll << 56) return DSPARK_ERR_INVALID_ARG;
+      if (counts[i] == 0) continue;
+      const int64_t size = dtypes[i] == DSPARK_DTYPE_BF16 ? 2 : 4;
+      if (!grads[i] || !outs[i] || !aligned_to(grads[i], size) || !aligned_to(outs[i], size))
+        return DSPARK_ERR_INVALID_ARG;
+      const uintptr_t g = reinterpret_cast<uintptr_t>(grads[i]), o = reinterpret_cast<uintptr_t>(outs[i]);
+      ranges.push_back({g, g + (uintptr_t)(counts[i] * size)});
+      if (o != g) ranges.push_back({o, o + (uintptr_t)(counts[i] * size)});
+      const int64_t per = kClipPieceBytes / size;
+      for (int64_t at = 0; at < counts[i]; at += per, ++n) {
+        if (!plan) continue;
+        if (n >= capacity) return DSPARK_ERR_INVALID_ARG;
+        plan[n].grad = static_cast<const char*>(grads[i]) + at * size;
+        plan[n].out = static_cast<char*>(outs[i]) + at * size;
+        plan[n].count = (int32_t)(counts[i] - at < per ? counts[i] - at : per);
+        plan[n].dtype = dtypes[i];
+      }
+    }
+    std::sort(ranges.begin(), ranges.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+    for (size_t i = 1; i < ranges.size(); ++i)
+      if (ranges[i].lo < ranges[i - 1].hi) return DSPARK_ERR_INVALID_ARG;
+    *pieces = n;
+  } catch (const std::bad_alloc&) {
+    return DSPARK_ERR_UNSUPPORTED;
+  } catch (const std::length_error&) {
+    return DSPARK_ERR_UNSUPPORTED;
+  }
+  return DSPARK_OK;
+}
+
+int dspark_markov_clip_grad_norm(const dspark_markov_clip_piece* plan, int64_t pieces, float max_norm, float* norm,
+                                 void* scratch, void* stream) {
+  t_last_algo = 0;
+  t_last_variant = 0;
+  static_assert(DSPARK_CLIP_MAX_PARTIALS * sizeof(double) <= DSPARK_CLIP_SCRATCH_BYTES, "partials fit the scratch");
+  if (pieces < 0 || !(max_norm >= 0.0f) || !norm || !scratch || !aligned_to(scratch, 8) || (pieces > 0 && !plan))
+    return DSPARK_ERR_INVALID_ARG;
+  int err = DSPARK_OK;
+  DeviceState* d = device_state(&err);
+  if (!d) return err;
+  ClipArgs a{plan, pieces, max_norm, norm, static_cast<double*>(scratch)};
+  t_last_algo = 1;
+  return cuda_code(launch_clip(a, d->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 int dspark_markov_get_status(void* stream, int32_t* status_out) {

@@ -68,6 +68,7 @@ struct __align__(64) ApplyMaps {
 
 struct ApplyParams {
   const int64_t* ids;
+  int64_t ld_id;  // the id of row i at ids[i * ld_id]
   const __nv_bfloat16* w1;
   int64_t rows, vocab;
   int32_t rank;
@@ -156,7 +157,7 @@ __device__ __forceinline__ void gather_tile_to_tmem(const ApplyParams& p, int m,
   const int64_t grow = (int64_t)m * kBM + row;
   int64_t id = -1;
   if (grow < p.rows) {
-    id = p.ids[grow];
+    id = p.ids[grow * p.ld_id];
     if (id < 0 || id >= p.vocab) {
       report_status(p.status, DSPARK_STATUS_TOKEN_RANGE);
       id = -1;
@@ -570,13 +571,15 @@ cudaError_t launch_ka(const TcApplyArgs& a, int num_sms, cudaStream_t stream) {
   const bool f32 = a.logits_f32 != 0;
   const CUtensorMapDataType ldt = f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const uint64_t ldim[2] = {(uint64_t)a.vocab, (uint64_t)a.rows};
-  const uint64_t lstr[1] = {(uint64_t)a.vocab * (f32 ? 4 : 2)};
+  const uint64_t in_str[1] = {(uint64_t)(a.ld_in ? a.ld_in : a.vocab) * (f32 ? 4 : 2)};
+  const uint64_t out_str[1] = {(uint64_t)(a.ld_out ? a.ld_out : a.vocab) * (f32 ? 4 : 2)};
   const uint32_t ubox[2] = {f32 ? 32u : 64u, 128};  // 128-byte rows
   const uint32_t lbox[2] = {64, 128};
   const bool has_base = a.base != nullptr;
   // Without a base the U map is never read; it is encoded on `out` to stay valid.
-  if (!encode_tensor_map(&maps.u, ldt, 2, has_base ? a.base : a.out, ldim, lstr, ubox, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_tensor_map(&maps.out, ldt, 2, a.out, ldim, lstr, ubox, CU_TENSOR_MAP_SWIZZLE_128B))
+  if (!encode_tensor_map(&maps.u, ldt, 2, has_base ? a.base : a.out, ldim, has_base ? in_str : out_str, ubox,
+                         CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tensor_map(&maps.out, ldt, 2, a.out, ldim, out_str, ubox, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   const uint64_t wdim[2] = {(uint64_t)a.rank, (uint64_t)a.vocab};
   const uint64_t wstr[1] = {(uint64_t)a.rank * 2};
@@ -586,6 +589,7 @@ cudaError_t launch_ka(const TcApplyArgs& a, int num_sms, cudaStream_t stream) {
 
   ApplyParams p{};
   p.ids = a.ids;
+  p.ld_id = a.ld_id ? a.ld_id : 1;
   p.w1 = static_cast<const __nv_bfloat16*>(a.w1);
   p.rows = a.rows;
   p.vocab = a.vocab;

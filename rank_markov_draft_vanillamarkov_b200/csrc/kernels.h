@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "../../include/dspark_markov.h"
+
 namespace dspark {
 
 // Counts kernel launches made by this library (dspark_markov_launch_count).
@@ -70,6 +72,8 @@ struct TcApplyArgs {
   uint32_t* status;
   uint64_t wait_limit_ns;
   int32_t logits_f32;  // base/out are fp32 (else bf16); the weights are bf16
+  // Row strides of base, out (elements; 0 means vocab) and ids (0 means 1).
+  int64_t ld_in, ld_out, ld_id;
 };
 bool tc_apply_supported(int64_t rows, int64_t vocab, int32_t rank, int logits_dtype, int weight_dtype);
 cudaError_t launch_tc_apply(const TcApplyArgs& a, int num_sms, cudaStream_t s);
@@ -143,6 +147,66 @@ struct TcFusedArgs {
 bool tc_fused_supported(int64_t rows, int64_t hidden_dim, int64_t vocab, int32_t rank, int out_dtype,
                         int weight_dtype);
 cudaError_t launch_tc_fused(const TcFusedArgs& a, int num_sms, cudaStream_t s);
+
+// ------------------------------------------- constraints, loss, clipping --
+// Token constraints on logits [batch, block, vocab] (constraints.cu). Strides
+// are in elements; tables are [batch, ...].
+struct ConstrainArgs {
+  const void* in;
+  void* out;
+  int64_t batch, block, vocab;
+  int64_t in_batch, in_row, out_batch, out_row;
+  const int64_t* history;
+  int64_t history_cap, history_stride;
+  const int64_t* history_lens;
+  const int64_t* prompt_lens;
+  const float *repetition, *frequency, *presence;  // [batch], or null for the values below
+  float repetition_value, frequency_value, presence_value;
+  const int64_t* bias_ids;
+  const float* bias_values;
+  int64_t bias_count, bias_stride;
+  const int64_t* draft;  // drafted tokens [batch, ...]; row k follows the first draft_first + k of them
+  int64_t draft_stride, draft_first;
+  const uint32_t* allowed;  // bit v of a row's words, or null
+  int64_t allowed_batch, allowed_row;
+  unsigned long long* keys;  // scratch of constrain_key_count() keys, or null: no tokens wanted
+  int64_t* tokens;
+  int64_t tokens_batch;  // the token of row (b, k) at tokens[b * tokens_batch + k]
+  int32_t greedy;
+  float temperature;
+  uint64_t seed;
+  uint32_t* status;
+};
+// Upper bound of the keys that a call of these sizes uses.
+int64_t constrain_key_count(int64_t batch, int64_t block, int64_t vocab);
+cudaError_t launch_constrain(const ConstrainArgs& a, int logits_dtype, int num_sms, cudaStream_t s);
+
+// The training loss and its gradient (loss.cu).
+struct LossArgs {
+  const void* logits;      // [rows, vocab]
+  const int64_t* targets;  // [rows]
+  const float* weights;    // [rows] or null (all one)
+  int64_t rows, vocab;
+  int64_t ignore_index;
+  int32_t mean;
+  float* loss;        // one element
+  float* row_losses;  // [rows]
+  void* grad;         // [rows, vocab] or null; may be logits
+  void* scratch;      // DSPARK_LOSS_SCRATCH_BYTES
+  uint32_t* status;
+};
+cudaError_t launch_loss(const LossArgs& a, int logits_dtype, int num_sms, cudaStream_t s);
+
+// Gradient clipping over a plan's pieces (clip.cu), each at most kClipPieceBytes.
+constexpr int64_t kClipPieceBytes = 65536;
+struct ClipArgs {
+  const dspark_markov_clip_piece* plan;  // device memory
+  int64_t pieces;
+  float max_norm;
+  float* norm;       // one element
+  double* partials;  // DSPARK_CLIP_MAX_PARTIALS elements
+};
+cudaError_t launch_clip(const ClipArgs& a, int num_sms, cudaStream_t s);
 
 // Encodes a tiled TMA descriptor through the driver entry point.
 bool encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t rank, const void* base,

@@ -14,6 +14,7 @@ predecessor (``apply_block_logits``); inference samples left to right
 """
 from __future__ import annotations
 
+import contextlib
 import functools
 import math
 import os
@@ -49,6 +50,14 @@ def _ranged(fn):
 
 def _stream_ptr(device: torch.device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
+
+
+_NO_GUARD = contextlib.nullcontext()
+
+
+def _device_guard(device: torch.device):
+    """Makes `device` the current one for a call into the library, which launches there."""
+    return _NO_GUARD if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def _check_cuda(t: torch.Tensor, name: str, device: torch.device) -> None:
@@ -214,6 +223,39 @@ class VanillaMarkov:
         return outs[0], outs[1]
 
     @_ranged
+    def teacher_forced_gradients(self, base_logits: torch.Tensor, *, token_ids: torch.Tensor, targets: torch.Tensor,
+                                 weights: Optional[torch.Tensor] = None, ignore_index: int = -100,
+                                 reduction: str = "mean", corrected: Optional[torch.Tensor] = None,
+                                 grad_w1: Optional[torch.Tensor] = None, grad_w2: Optional[torch.Tensor] = None,
+                                 max_norm: Optional[float] = None, clipper=None):
+        """One teacher-forced training step up to the update: the corrected
+        logits of ``base_logits`` (..., M, V) after ``token_ids`` (..., M), their
+        cross entropy against ``targets`` (..., M) (training.block_cross_entropy)
+        and the gradients of W1 and W2 (into ``grad_w1`` and ``grad_w2`` if
+        given), clipped to a norm of ``max_norm`` unless that is None.
+        ``clipper`` is a GradientClipper over the given gradient buffers and
+        whatever else is clipped with them, for steps that keep their buffers;
+        without one the two gradients are clipped by their own joint norm.
+        Returns a dict: ``loss``, ``row_losses``, ``grad_logits`` (the gradient
+        of the base logits, unclipped; it takes the corrected logits' buffer,
+        ``corrected`` if given), ``grad_w1``, ``grad_w2`` and ``norm`` (None
+        without ``max_norm``)."""
+        from .training import block_cross_entropy, clip_grad_norm
+        if base_logits.numel() == 0:
+            raise ValueError("base_logits is empty")
+        if clipper is not None and (grad_w1 is None or grad_w2 is None or max_norm is None):
+            raise ValueError("clipper needs max_norm and the gradient buffers that it was made for")
+        out = self.apply_block_logits(base_logits, token_ids=token_ids, out=corrected)
+        loss, row_losses, grad = block_cross_entropy(out, targets, weights=weights, ignore_index=ignore_index,
+                                                     reduction=reduction, out_grad=out)
+        gw1, gw2 = self.apply_block_logits_backward(grad, token_ids=token_ids, grad_w1=grad_w1, grad_w2=grad_w2)
+        norm = None
+        if max_norm is not None:
+            norm = clipper.clip(max_norm) if clipper is not None else clip_grad_norm([gw1, gw2], max_norm)
+        return {"loss": loss, "row_losses": row_losses, "grad_logits": grad, "grad_w1": gw1, "grad_w2": gw2,
+                "norm": norm}
+
+    @_ranged
     def transition_logits(self, token_ids: torch.Tensor, *, with_embeddings: bool = True,
                           out: Optional[torch.Tensor] = None,
                           out_embeddings: Optional[torch.Tensor] = None):
@@ -253,13 +295,21 @@ class VanillaMarkov:
     def sample_block_tokens(self, base_logits: torch.Tensor, *, first_prev_token_ids: torch.Tensor,
                             hidden_states: Optional[torch.Tensor] = None, temperature: Optional[float] = 0.0,
                             seed: int = 0, out_tokens: Optional[torch.Tensor] = None,
-                            out_logits: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+                            out_logits: Optional[torch.Tensor] = None, constraints=None,
+                            allowed: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
         """Left-to-right sampling of ``base_logits`` (B, M, V). Returns
         (sampled_tokens (B, M) int64, corrected_logits (B, M, V)). With M == 0
         returns an empty (B, 0) token tensor and ``base_logits`` itself.
         ``temperature`` None or below 1e-5 is greedy; otherwise each token is
         a Gumbel-max draw from softmax(c / T) with Philox noise keyed by
-        ``seed``. ``hidden_states`` is accepted and ignored."""
+        ``seed``. ``hidden_states`` is accepted and ignored.
+
+        With ``constraints`` (a TokenConstraints) or ``allowed`` (int32 bit
+        masks (B, W) or (B, M, W), see process_logits) every position's
+        corrected logits go through process_logits, with the block's own
+        earlier tokens as the drafted ones, before the choice; the returned
+        logits are the constrained ones. That runs a correction and a
+        constraint step per position instead of one persistent kernel."""
         del hidden_states
         if base_logits.dim() != 3:
             raise ValueError("base_logits must be (B, M, V)")
@@ -281,11 +331,38 @@ class VanillaMarkov:
             raise ValueError("temperature is NaN")
         tokens = out_tokens if out_tokens is not None else torch.empty(batch, m, dtype=torch.long, device=self.device)
         corrected = out_logits if out_logits is not None else torch.empty_like(base_logits)
+        if constraints is not None or allowed is not None:
+            return self._sample_constrained(base_logits, prev, t, seed, tokens, corrected, constraints, allowed)
         code = self._lib.dspark_markov_sample_block(
             base_logits.data_ptr(), prev.data_ptr(), batch, m, vocab, self.markov_w1.data_ptr(),
             self.markov_w2.data_ptr(), self.markov_rank, t, seed & 0xFFFFFFFFFFFFFFFF, tokens.data_ptr(),
             corrected.data_ptr(), _DT[base_logits.dtype], _DT[self.weight_dtype], _stream_ptr(self.device))
         N.check(code, "dspark_markov_sample_block")
+        return tokens, corrected
+
+    def _sample_constrained(self, base_logits, prev, temperature, seed, tokens, corrected, constraints, allowed):
+        from .constraints import TokenConstraints, _allowed_args
+        batch, m, vocab = base_logits.shape
+        constraints = constraints if constraints is not None else TokenConstraints(vocab)
+        constraints._check(batch, vocab, self.device)
+        mask, mask_batch, mask_row = _allowed_args(allowed, batch, m, vocab, self.device)
+        if tuple(tokens.shape) != (batch, m) or tokens.dtype != torch.int64:
+            raise ValueError("out_tokens must be int64 (B, M)")
+        if corrected.shape != base_logits.shape or corrected.dtype != base_logits.dtype:
+            raise ValueError("out_logits must match base_logits in shape and dtype")
+        _check_cuda(tokens, "out_tokens", self.device)
+        _check_cuda(corrected, "out_logits", self.device)
+        if batch == 0:
+            return tokens, corrected
+        with _device_guard(self.device):
+            scratch = torch.empty(self._lib.dspark_markov_constrain_scratch_bytes(batch, 1, vocab),
+                                  dtype=torch.uint8, device=self.device)
+            code = self._lib.dspark_markov_sample_block_constrained(
+                base_logits.data_ptr(), prev.data_ptr(), batch, m, vocab, self.markov_w1.data_ptr(),
+                self.markov_w2.data_ptr(), self.markov_rank, temperature, seed & 0xFFFFFFFFFFFFFFFF, constraints._ref,
+                mask, mask_batch, mask_row, tokens.data_ptr(), corrected.data_ptr(), scratch.data_ptr(),
+                _DT[base_logits.dtype], _DT[self.weight_dtype], _stream_ptr(self.device))
+        N.check(code, "dspark_markov_sample_block_constrained")
         return tokens, corrected
 
     @_ranged

@@ -1,0 +1,150 @@
+"""What a training step runs around the head: the teacher-forced loss with its
+gradient, and the global gradient norm with clipping.
+
+A step is ``apply_block_logits`` -> ``block_cross_entropy`` ->
+``apply_block_logits_backward`` -> (the all-reduce of ``sharding``) ->
+``GradientClipper.clip``; ``VanillaMarkov.teacher_forced_gradients`` runs it.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Optional, Sequence, Tuple
+
+import torch
+
+from . import _native as N
+from .head import _DT, _check_cuda, _device_guard, _ranged, _stream_ptr
+
+
+@_ranged
+def block_cross_entropy(logits: torch.Tensor, targets: torch.Tensor, *, weights: Optional[torch.Tensor] = None,
+                        ignore_index: int = -100, reduction: str = "mean", want_grad: bool = True,
+                        out_grad: Optional[torch.Tensor] = None
+                        ) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor]]:
+    """Cross entropy of corrected ``logits`` (..., V) against ``targets`` (...)
+    int64, with its gradient. Returns (loss, row_losses, grad):
+
+        row_losses[i] = logsumexp(logits[i]) - logits[i, targets[i]]           fp32 (...)
+        loss          = sum_i weights[i] row_losses[i] / N                     fp32 scalar
+        grad[i]       = weights[i] / N (softmax(logits[i]) - onehot(targets[i]))
+
+    N is the sum of the weights of the rows that count ("mean") or 1 ("sum").
+    ``weights`` (...) fp32 (default all 1; a block's later positions or other
+    losses' shares). A row whose target is ``ignore_index`` or whose weight is
+    zero does not count: its logits are not read, its loss and gradient are 0.
+    A target outside the vocabulary does the same and sets the TOKEN_RANGE
+    status bit. With no row left the loss is 0. ``out_grad`` takes the gradient
+    (the logits' shape and dtype) and may be ``logits`` (in place); the
+    gradient is the ``grad_out`` of ``apply_block_logits_backward``."""
+    if logits.dim() < 1:
+        raise ValueError("logits must be (..., V)")
+    dtype, device = logits.dtype, logits.device
+    if dtype not in _DT:
+        raise ValueError("logits must be float32 or bfloat16")
+    if reduction not in ("mean", "sum"):
+        raise ValueError("reduction must be 'mean' or 'sum'")
+    vocab = logits.shape[-1]
+    if vocab == 0:
+        raise ValueError("logits must have a vocabulary")
+    lead = logits.shape[:-1]
+    if targets.shape != lead:
+        raise ValueError("targets must match logits without its last dim")
+    ids = targets if targets.dtype == torch.int64 else targets.long()
+    _check_cuda(logits, "logits", device)
+    _check_cuda(ids, "targets", device)
+    if weights is not None:
+        if weights.shape != lead or weights.dtype != torch.float32:
+            raise ValueError("weights must be fp32 with the shape of targets")
+        _check_cuda(weights, "weights", device)
+    grad = None
+    if out_grad is not None:
+        if out_grad is not logits:
+            if out_grad.shape != logits.shape or out_grad.dtype != dtype:
+                raise ValueError("out_grad must match logits in shape and dtype")
+            _check_cuda(out_grad, "out_grad", device)
+        grad = out_grad
+    elif want_grad:
+        grad = torch.empty_like(logits)
+    rows = ids.numel()
+    lib = N.load()
+    with _device_guard(device):
+        loss = torch.empty((), dtype=torch.float32, device=device)
+        row_losses = torch.empty(lead, dtype=torch.float32, device=device)
+        scratch = torch.empty(N.DSPARK_LOSS_SCRATCH_BYTES, dtype=torch.uint8, device=device)
+        code = lib.dspark_markov_block_cross_entropy(
+            logits.data_ptr(), ids.data_ptr(), weights.data_ptr() if weights is not None else None, rows, vocab,
+            ignore_index, reduction == "mean", loss.data_ptr(), row_losses.data_ptr(),
+            grad.data_ptr() if grad is not None else None, scratch.data_ptr(), _DT[dtype], _stream_ptr(device))
+    N.check(code, "dspark_markov_block_cross_entropy")
+    return loss, row_losses, grad
+
+
+class GradientClipper:
+    """The global norm over ``grads`` and clipping by it, for buffers that stay
+    where they are from step to step (a flat bucket's views, the head's dW1 and
+    dW2).
+
+    ``grads``: contiguous fp32 or bf16 CUDA tensors on one device that do not
+    overlap. ``out``: tensors of the same shapes and dtypes that take the
+    clipped gradients (each its gradient itself or memory that overlaps none of
+    them); None: in place. Creating the object lays the tensors out as a plan
+    in device memory (a host-to-device copy: create it before a graph capture);
+    ``clip`` reads what the tensors hold at each call.
+    """
+
+    def __init__(self, grads: Sequence[torch.Tensor], *, out: Optional[Sequence[torch.Tensor]] = None):
+        grads = list(grads)
+        outs = grads if out is None else list(out)
+        if len(outs) != len(grads):
+            raise ValueError("out must have one tensor for each gradient")
+        self.device = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
+        for i, (g, o) in enumerate(zip(grads, outs)):
+            if g.dtype not in _DT:
+                raise ValueError("gradients must be float32 or bfloat16")
+            if o.shape != g.shape or o.dtype != g.dtype:
+                raise ValueError("out must match the gradients in shape and dtype")
+            _check_cuda(g, f"grads[{i}]", self.device)
+            if o is not g:
+                _check_cuda(o, f"out[{i}]", self.device)
+        self.grads, self.outs = grads, outs
+        lib = N.load()
+        n = len(grads)
+        args = ((ctypes.c_void_p * n)(*[g.data_ptr() for g in grads]), (ctypes.c_void_p * n)(*[o.data_ptr() for o in outs]),
+                (ctypes.c_int64 * n)(*[g.numel() for g in grads]), (ctypes.c_int32 * n)(*[_DT[g.dtype] for g in grads]), n)
+        pieces = ctypes.c_int64(0)
+        self._checked(lib.dspark_markov_clip_plan(*args, None, 0, ctypes.byref(pieces)))
+        self._pieces = pieces.value
+        plan = (N.ClipPiece * max(1, self._pieces))()
+        self._checked(lib.dspark_markov_clip_plan(*args, plan, self._pieces, ctypes.byref(pieces)))
+        self._plan = torch.frombuffer(plan, dtype=torch.uint8).to(self.device)
+
+    @staticmethod
+    def _checked(code: int) -> None:
+        if code == N.DSPARK_ERR_INVALID_ARG:
+            raise ValueError("gradients and outputs must not overlap one another")
+        N.check(code, "dspark_markov_clip_plan")
+
+    @_ranged
+    def clip(self, max_norm: float) -> torch.Tensor:
+        """Scales by min(1, max_norm / (norm + 1e-6)) and returns the norm before
+        it, an fp32 scalar on the device. ``max_norm`` inf only measures (and
+        copies to ``out``). An infinite norm scales by 0 and a NaN norm by NaN."""
+        max_norm = float(max_norm)
+        if math.isnan(max_norm) or max_norm < 0.0:
+            raise ValueError("max_norm must not be negative or NaN")
+        device = self.device
+        with _device_guard(device):
+            norm = torch.empty((), dtype=torch.float32, device=device)
+            scratch = torch.empty(N.DSPARK_CLIP_SCRATCH_BYTES, dtype=torch.uint8, device=device)
+            code = N.load().dspark_markov_clip_grad_norm(self._plan.data_ptr(), self._pieces, max_norm,
+                                                         norm.data_ptr(), scratch.data_ptr(), _stream_ptr(device))
+        N.check(code, "dspark_markov_clip_grad_norm")
+        return norm
+
+
+def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, *,
+                   out: Optional[Sequence[torch.Tensor]] = None) -> torch.Tensor:
+    """``GradientClipper(grads, out=out).clip(max_norm)`` for buffers that are
+    clipped once."""
+    return GradientClipper(grads, out=out).clip(max_norm)

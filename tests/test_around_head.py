@@ -1,0 +1,185 @@
+"""What needs no GPU of the operators around the head: the 64-bit forms against hand-worked values, the clip plan and
+the refusals of the C entries (no device call is made before them)."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import around
+from rank_markov_draft_vanillamarkov_b200 import TokenConstraints, _native as N, block_cross_entropy, clip_grad_norm
+from rank_markov_draft_vanillamarkov_b200 import build as B
+from rank_markov_draft_vanillamarkov_b200 import constraints as C, training as T
+from rank_markov_draft_vanillamarkov_b200.head import VanillaMarkov
+
+
+@pytest.fixture(scope="module")
+def lib():
+    B.build()
+    return N.load()
+
+
+def test_constrain_row_by_hand():
+    row = [2.0, -2.0, 3.0, 0.5, 1.0]
+    x, err = around.constrain_row(row, [0, 1], [2, 2, 0], 2.0, 0.25, 0.5, [(3, 1.0), (-1, 9.0), (3, -0.25)],
+                                  np.array([True, True, True, True, False]))
+    # 0: 2/2 - 0.25 - 0.5; 1: -2*2; 2: 3/2 - 0.5 - 0.5; 3: 0.5 - 0.25; 4: masked
+    assert x.tolist() == [0.25, -4.0, 0.5, 0.25, -math.inf]
+    assert err[4] == 0 and err[0] > 0
+    assert around.choose(x) == 2 and around.choose([1.0, float("nan"), 2.0]) == 1 and around.choose([3.0, 3.0]) == 0
+    assert around.choose([-math.inf] * 3) == 0
+
+
+def test_allowed_words():
+    words = np.array([[5, 1]], dtype=np.int32)
+    assert np.flatnonzero(around.allowed_from_words(words, 40)[0]).tolist() == [0, 2, 32]
+    assert around.allowed_from_words(np.array([-(1 << 31)], dtype=np.int32), 32)[31]
+
+
+def test_cross_entropy_by_hand_and_differences():
+    x = np.log(np.array([[1.0, 3.0], [2.0, 2.0], [1.0, 1.0]]))
+    (loss, _), (rows, _), (grad, _) = around.cross_entropy(x, [1, 0, -100], [2.0, 1.0, 5.0], -100, True, "fp32")
+    assert rows == pytest.approx([math.log(4 / 3), math.log(2), 0.0])
+    assert loss == pytest.approx((2 * math.log(4 / 3) + math.log(2)) / 3)
+    assert grad == pytest.approx(np.array([[0.5 / 3, -0.5 / 3], [-0.5 / 3, 0.5 / 3], [0, 0]]))
+    g = np.random.default_rng(0)
+    x, t, h = g.normal(0, 2, (4, 9)), [3, 0, 8, 2], 1e-5
+    grad = around.cross_entropy(x, t, None, -100, False, "fp32")[2][0]
+    for i in range(4):
+        for v in range(9):
+            d = np.zeros_like(x)
+            d[i, v] = h
+            up, dn = (around.cross_entropy(x + s * d, t, None, -100, False, "fp32")[0][0] for s in (1, -1))
+            assert abs((up - dn) / (2 * h) - grad[i, v]) <= 1e-8
+
+
+def _plan(lib, spans, capacity=None):
+    n = len(spans)
+    pieces = ctypes.c_int64(-1)
+    args = ((ctypes.c_void_p * n)(*[s[0] for s in spans]), (ctypes.c_void_p * n)(*[s[1] for s in spans]),
+            (ctypes.c_int64 * n)(*[s[2] for s in spans]), (ctypes.c_int32 * n)(*[s[3] for s in spans]), n)
+    code = lib.dspark_markov_clip_plan(*args, None, 0, ctypes.byref(pieces))
+    if code != N.DSPARK_OK:
+        return code, None
+    plan = (N.ClipPiece * max(1, pieces.value))()
+    code = lib.dspark_markov_clip_plan(*args, plan, pieces.value if capacity is None else capacity,
+                                       ctypes.byref(pieces))
+    return code, [(p.grad, p.out, p.count, p.dtype) for p in plan[: pieces.value]]
+
+
+def test_clip_plan_covers_every_element_once(lib):
+    spans = [(1 << 20, 1 << 20, 40001, 1), (1 << 24, 1 << 26, 16384, 0), (0, 0, 0, 0), (1 << 28, 1 << 28, 1, 1),
+             ((1 << 30) + 4, (1 << 32) + 8, 16385, 0)]
+    code, pieces = _plan(lib, spans)
+    assert code == N.DSPARK_OK
+    for grad, out, count, dtype in spans:
+        if not count:
+            continue
+        size = 2 if dtype else 4
+        mine = [p for p in pieces if grad <= p[0] < grad + count * size]
+        assert sum(p[2] for p in mine) == count and all(p[3] == dtype and p[2] > 0 for p in mine)
+        at = 0
+        for p in mine:
+            assert p[0] == grad + at * size and p[1] == out + at * size
+            at += p[2]
+    assert _plan(lib, [])[1] == []
+
+
+def test_clip_plan_refusals(lib):
+    ok = (1 << 20, 1 << 20, 100, 0)
+    assert _plan(lib, [ok, ((1 << 20) + 396, 1 << 30, 10, 0)])[0] == N.DSPARK_ERR_INVALID_ARG  # overlap
+    assert _plan(lib, [ok, ok])[0] == N.DSPARK_ERR_INVALID_ARG  # the same tensor twice
+    assert _plan(lib, [ok, ((1 << 20) + 400, 1 << 30, 10, 0)])[0] == N.DSPARK_OK  # neighbours
+    assert _plan(lib, [(1 << 20, (1 << 20) + 4, 100, 0)])[0] == N.DSPARK_ERR_INVALID_ARG
+    assert _plan(lib, [(1 << 20, 1 << 20, -1, 0)])[0] == N.DSPARK_ERR_INVALID_ARG
+    assert _plan(lib, [(1 << 20, 1 << 20, 1, 3)])[0] == N.DSPARK_ERR_INVALID_ARG
+    assert _plan(lib, [(0, 0, 1, 0)])[0] == N.DSPARK_ERR_INVALID_ARG
+    assert _plan(lib, [((1 << 20) + 2, (1 << 20) + 2, 1, 0)])[0] == N.DSPARK_ERR_INVALID_ARG  # misaligned
+    assert _plan(lib, [ok], capacity=0)[0] == N.DSPARK_ERR_INVALID_ARG
+
+
+def test_c_entry_refusals(lib):
+    p, bad, ok = ctypes.c_void_p(1 << 20), N.DSPARK_ERR_INVALID_ARG, N.DSPARK_OK  # never dereferenced
+    far = ctypes.c_void_p(1 << 40)
+    c = N.Constraints()
+    c.repetition_value = 1.0
+    ref = ctypes.byref(c)
+    pr = lib.dspark_markov_process_logits
+
+    def process(x=p, out=far, b=2, m=3, v=64, ib=192, ir=64, ob=192, orow=64, con=ref, draft=None, ds=3, first=0,
+                al=None, tok=None, ts=3, temp=0.0, scratch=None, dt=0):
+        return pr(x, out, b, m, v, ib, ir, ob, orow, con, draft, ds, first, al, 0, 0, tok, ts, temp, 0, scratch, dt,
+                  None)
+
+    assert process(b=0) == ok and process(m=0) == ok
+    assert process(b=-1) == bad and process(v=0) == bad and process(dt=2) == bad and process(con=None) == bad
+    assert process(x=None) == bad and process(out=None) == bad and process(tok=p) == bad  # tokens without scratch
+    assert process(temp=float("nan")) == bad and process(ib=-1) == bad and process(first=-1) == bad
+    assert process(ob=100) == bad and process(orow=63) == bad and process(ob=0) == bad  # rows that overlap
+    assert process(out=p, orow=64, ob=200) == bad  # in place with other strides
+    assert process(out=ctypes.c_void_p((1 << 20) + 256)) == bad  # another overlap
+    assert process(x=ctypes.c_void_p((1 << 20) + 2)) == bad and process(scratch=ctypes.c_void_p(4)) == bad
+    assert process(tok=p, scratch=far, ts=2) == bad and process(draft=p, ds=1) == bad
+    assert process(v=1 << 33, ib=0, ir=0, ob=1 << 40, orow=1 << 35) == N.DSPARK_ERR_UNSUPPORTED
+    assert process(b=1 << 20, m=1 << 20) == N.DSPARK_ERR_UNSUPPORTED
+    for field, value in (("history_cap", -1), ("bias_count", 2), ("bias_stride", -1), ("history_stride", -1)):
+        d = N.Constraints()
+        setattr(d, field, value)
+        assert process(con=ctypes.byref(d)) == bad, field
+    size = lib.dspark_markov_constrain_scratch_bytes
+    assert size(2, 3, 64) >= 48 and size(0, 3, 64) == 0 and size(2, 3, 0) == 0 and size(1 << 20, 1 << 20, 64) == 0
+    sm = lib.dspark_markov_sample_block_constrained
+
+    def sample(base=p, out=far, b=2, m=3, rank=16, temp=0.0, con=ref, scratch=far, ldt=0):
+        return sm(base, p, b, m, 64, p, p, rank, temp, 0, con, None, 0, 0, p, out, scratch, ldt, 0, None)
+
+    assert sample(b=0) == ok and sample(m=0) == ok
+    assert sample(rank=0) == bad and sample(con=None) == bad and sample(scratch=None) == bad and sample(ldt=5) == bad
+    assert sample(temp=float("nan")) == bad and sample(out=p) == bad and sample(b=-1) == bad
+    ce = lib.dspark_markov_block_cross_entropy
+
+    def entropy(x=p, t=p, rows=4, v=10, loss=p, row=p, grad=far, scratch=far, dt=0):
+        return ce(x, t, None, rows, v, -100, 1, loss, row, grad, scratch, dt, None)
+
+    assert entropy(x=None) == bad and entropy(t=None) == bad and entropy(loss=None) == bad and entropy(v=0) == bad
+    assert entropy(rows=-1) == bad and entropy(dt=7) == bad and entropy(scratch=None) == bad and entropy(row=None) == bad
+    assert entropy(grad=ctypes.c_void_p((1 << 20) + 16)) == bad and entropy(grad=ctypes.c_void_p((1 << 40) + 2)) == bad
+    assert entropy(rows=1 << 40) == N.DSPARK_ERR_UNSUPPORTED
+    cl = lib.dspark_markov_clip_grad_norm
+    assert cl(None, 1, 1.0, p, p, None) == bad and cl(p, -1, 1.0, p, p, None) == bad
+    assert cl(p, 1, -1.0, p, p, None) == bad and cl(p, 1, float("nan"), p, p, None) == bad
+    assert cl(p, 1, 1.0, None, p, None) == bad and cl(p, 1, 1.0, p, None, None) == bad
+
+
+def test_structs_match_the_header():
+    # The library asserts the same sizes when it is compiled: eight 8-byte fields, three floats and their padding,
+    # four 8-byte fields; two pointers and two 4-byte fields.
+    assert ctypes.sizeof(N.Constraints) == 112 and ctypes.sizeof(N.ClipPiece) == 24
+    text = open(B.ROOT + "/include/dspark_markov.h").read()
+    for name in ("DSPARK_LOSS_SCRATCH_BYTES", "DSPARK_CLIP_MAX_PARTIALS", "DSPARK_CLIP_SCRATCH_BYTES"):
+        assert f"#define {name} {getattr(N, name)}\n" in text
+
+
+def test_python_refusals_without_a_gpu():
+    with pytest.raises(ValueError):
+        TokenConstraints(0)
+    with pytest.raises(ValueError):
+        TokenConstraints(10, repetition_penalty=0.0)
+    with pytest.raises(ValueError):
+        TokenConstraints(10, frequency_penalty=math.inf)
+    with pytest.raises(ValueError):
+        TokenConstraints(10, history_lens=torch.zeros(2, dtype=torch.int64))
+    with pytest.raises(ValueError):
+        TokenConstraints(10, history=torch.zeros(2, 3, dtype=torch.int64))  # not on a GPU
+    with pytest.raises(ValueError):
+        block_cross_entropy(torch.zeros(2, 5), torch.zeros(2, dtype=torch.int64))
+    with pytest.raises(ValueError):
+        clip_grad_norm([torch.zeros(3)], 1.0)
+
+
+@pytest.mark.parametrize("fn,name", [(C.process_logits, "process_logits"), (T.block_cross_entropy, "block_cross_entropy"),
+                                     (T.GradientClipper.clip, "clip"),
+                                     (VanillaMarkov.teacher_forced_gradients, "teacher_forced_gradients")])
+def test_entry_points_are_ranged(fn, name):
+    assert fn.__wrapped__.__name__ == name
