@@ -346,18 +346,14 @@ int dspark_markov_sample_block_constrained(const void* base_logits, const int64_
  *   loss        one fp32 element, row_losses [rows] fp32, both written.
  *   grad        [rows, vocab] logits_dtype, written, or NULL (not wanted); may
  *               equal logits, other overlaps are DSPARK_ERR_INVALID_ARG.
- *   scratch     DSPARK_LOSS_SCRATCH_BYTES bytes of device memory, 8-byte
- *               aligned; calls that overlap take one each.
  *
  * Sums are fp32 or wider and in a fixed order; the gradient is rounded once. A
  * live row that holds NaN or +inf, or -inf everywhere, has a NaN loss and
  * gradient. rows == 0 writes loss = 0.
  */
-#define DSPARK_LOSS_SCRATCH_BYTES 64
 int dspark_markov_block_cross_entropy(const void* logits, const int64_t* targets, const float* weights, int64_t rows,
                                       int64_t vocab, int64_t ignore_index, int32_t mean, float* loss,
-                                      float* row_losses, void* grad, void* scratch, int32_t logits_dtype,
-                                      void* stream);
+                                      float* row_losses, void* grad, int32_t logits_dtype, void* stream);
 
 /*
  * The global norm over many gradient tensors and clipping by it:

@@ -38,7 +38,6 @@ DSPARK_VARIANT_BWD_RESIDENT_W1 = 1
 DSPARK_VARIANT_SAMPLE_ROWS = 2
 DSPARK_VARIANT_APPLY_WIDE = 4
 
-DSPARK_LOSS_SCRATCH_BYTES = 64
 DSPARK_CLIP_MAX_PARTIALS = 1024
 DSPARK_CLIP_SCRATCH_BYTES = 8192
 
@@ -77,7 +76,7 @@ SIGNATURES = {
     "dspark_markov_constrain_scratch_bytes": (_i64, [_i64, _i64, _i64]),
     "dspark_markov_sample_block_constrained": (ctypes.c_int, [_vp, _vp, _i64, _i64, _i64, _vp, _vp, _i32, _f32, _u64,
                                                               _vp, _vp, _i64, _i64, _vp, _vp, _vp, _i32, _i32, _vp]),
-    "dspark_markov_block_cross_entropy": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp,
+    "dspark_markov_block_cross_entropy": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _vp,
                                                          _i32, _vp]),
     "dspark_markov_clip_plan": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _vp, _i64, ctypes.POINTER(_i64)]),
     "dspark_markov_clip_grad_norm": (ctypes.c_int, [_vp, _i64, _f32, _vp, _vp, _vp]),

@@ -684,12 +684,10 @@ int dspark_markov_sample_block_constrained(const void* base_logits, const int64_
 
 int dspark_markov_block_cross_entropy(const void* logits, const int64_t* targets, const float* weights, int64_t rows,
                                       int64_t vocab, int64_t ignore_index, int32_t mean, float* loss,
-                                      float* row_losses, void* grad, void* scratch, int32_t logits_dtype,
-                                      void* stream) {
+                                      float* row_losses, void* grad, int32_t logits_dtype, void* stream) {
   t_last_algo = 0;
   t_last_variant = 0;
-  if (rows < 0 || vocab <= 0 || !dtype_ok(logits_dtype) || !loss || !scratch || !aligned_to(scratch, 8))
-    return DSPARK_ERR_INVALID_ARG;
+  if (rows < 0 || vocab <= 0 || !dtype_ok(logits_dtype) || !loss) return DSPARK_ERR_INVALID_ARG;
   if (rows > 0 && (!logits || !targets || !row_losses)) return DSPARK_ERR_INVALID_ARG;
   const size_t lsize = logits_dtype == DSPARK_DTYPE_BF16 ? 2 : 4;
   if (!aligned_to(logits, lsize) || !aligned_to(grad, lsize)) return DSPARK_ERR_INVALID_ARG;
@@ -702,8 +700,7 @@ int dspark_markov_block_cross_entropy(const void* logits, const int64_t* targets
   int err = DSPARK_OK;
   DeviceState* d = device_state(&err);
   if (!d) return err;
-  LossArgs a{logits, targets, weights, rows, vocab, ignore_index, mean ? 1 : 0, loss, row_losses, grad, scratch,
-             d->status};
+  LossArgs a{logits, targets, weights, rows, vocab, ignore_index, mean ? 1 : 0, loss, row_losses, grad, d->status};
   t_last_algo = 1;
   return cuda_code(launch_loss(a, logits_dtype, d->num_sms, static_cast<cudaStream_t>(stream)));
 }

@@ -192,7 +192,6 @@ struct LossArgs {
   float* loss;        // one element
   float* row_losses;  // [rows]
   void* grad;         // [rows, vocab] or null; may be logits
-  void* scratch;      // DSPARK_LOSS_SCRATCH_BYTES
   uint32_t* status;
 };
 cudaError_t launch_loss(const LossArgs& a, int logits_dtype, int num_sms, cudaStream_t s);

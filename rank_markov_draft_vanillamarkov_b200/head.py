@@ -48,7 +48,13 @@ def _ranged(fn):
     return wrapper
 
 
+# The current stream's handle, without the Stream object around it where torch offers that (0.1 against 2.2 us).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_ptr(device: torch.device) -> int:
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 

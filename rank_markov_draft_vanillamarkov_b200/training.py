@@ -71,11 +71,10 @@ def block_cross_entropy(logits: torch.Tensor, targets: torch.Tensor, *, weights:
     with _device_guard(device):
         loss = torch.empty((), dtype=torch.float32, device=device)
         row_losses = torch.empty(lead, dtype=torch.float32, device=device)
-        scratch = torch.empty(N.DSPARK_LOSS_SCRATCH_BYTES, dtype=torch.uint8, device=device)
         code = lib.dspark_markov_block_cross_entropy(
             logits.data_ptr(), ids.data_ptr(), weights.data_ptr() if weights is not None else None, rows, vocab,
             ignore_index, reduction == "mean", loss.data_ptr(), row_losses.data_ptr(),
-            grad.data_ptr() if grad is not None else None, scratch.data_ptr(), _DT[dtype], _stream_ptr(device))
+            grad.data_ptr() if grad is not None else None, _DT[dtype], _stream_ptr(device))
     N.check(code, "dspark_markov_block_cross_entropy")
     return loss, row_losses, grad
 

@@ -139,11 +139,11 @@ def test_c_entry_refusals(lib):
     assert sample(temp=float("nan")) == bad and sample(out=p) == bad and sample(b=-1) == bad
     ce = lib.dspark_markov_block_cross_entropy
 
-    def entropy(x=p, t=p, rows=4, v=10, loss=p, row=p, grad=far, scratch=far, dt=0):
-        return ce(x, t, None, rows, v, -100, 1, loss, row, grad, scratch, dt, None)
+    def entropy(x=p, t=p, rows=4, v=10, loss=p, row=p, grad=far, dt=0):
+        return ce(x, t, None, rows, v, -100, 1, loss, row, grad, dt, None)
 
     assert entropy(x=None) == bad and entropy(t=None) == bad and entropy(loss=None) == bad and entropy(v=0) == bad
-    assert entropy(rows=-1) == bad and entropy(dt=7) == bad and entropy(scratch=None) == bad and entropy(row=None) == bad
+    assert entropy(rows=-1) == bad and entropy(dt=7) == bad and entropy(row=None) == bad
     assert entropy(grad=ctypes.c_void_p((1 << 20) + 16)) == bad and entropy(grad=ctypes.c_void_p((1 << 40) + 2)) == bad
     assert entropy(rows=1 << 40) == N.DSPARK_ERR_UNSUPPORTED
     cl = lib.dspark_markov_clip_grad_norm
@@ -157,7 +157,7 @@ def test_structs_match_the_header():
     # four 8-byte fields; two pointers and two 4-byte fields.
     assert ctypes.sizeof(N.Constraints) == 112 and ctypes.sizeof(N.ClipPiece) == 24
     text = open(B.ROOT + "/include/dspark_markov.h").read()
-    for name in ("DSPARK_LOSS_SCRATCH_BYTES", "DSPARK_CLIP_MAX_PARTIALS", "DSPARK_CLIP_SCRATCH_BYTES"):
+    for name in ("DSPARK_CLIP_MAX_PARTIALS", "DSPARK_CLIP_SCRATCH_BYTES"):
         assert f"#define {name} {getattr(N, name)}\n" in text
 
 
