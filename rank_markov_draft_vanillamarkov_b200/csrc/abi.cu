@@ -700,7 +700,8 @@ int dspark_markov_block_cross_entropy(const void* logits, const int64_t* targets
   int err = DSPARK_OK;
   DeviceState* d = device_state(&err);
   if (!d) return err;
-  LossArgs a{logits, targets, weights, rows, vocab, ignore_index, mean ? 1 : 0, loss, row_losses, grad, d->status};
+  LossArgs a{logits, targets, weights, rows, vocab, ignore_index, mean ? 1 : 0, loss, row_losses, grad, d->status,
+             g_wait_limit_ns.load()};
   t_last_algo = 1;
   return cuda_code(launch_loss(a, logits_dtype, d->num_sms, static_cast<cudaStream_t>(stream)));
 }

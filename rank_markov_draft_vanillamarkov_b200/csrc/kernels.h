@@ -193,6 +193,7 @@ struct LossArgs {
   float* row_losses;  // [rows]
   void* grad;         // [rows, vocab] or null; may be logits
   uint32_t* status;
+  uint64_t wait_limit_ns;
 };
 cudaError_t launch_loss(const LossArgs& a, int logits_dtype, int num_sms, cudaStream_t s);
 

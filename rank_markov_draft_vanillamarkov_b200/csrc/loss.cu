@@ -5,31 +5,35 @@
 // (sum), d loss / d c_v = w_i / N (exp(c_v - lse) - [v = t]).
 //
 // The sum and the gradient both need the whole row, so a kernel that streams
-// reads it twice. Here a cluster of CTAs holds a row in its registers (a
-// 129280-id bf16 row is 252 KB, more than one SM's shared memory but an eighth
-// of a four-SM register file): each logit is read once and each gradient
-// written once, 4 bytes per bf16 logit, and that traffic is the bound.
+// reads it twice. Here a cluster of CTAs keeps a row in its shared memory (a
+// 129280-id bf16 row is 252 KB, more than one SM's): each logit is read once
+// and each gradient written once, 4 bytes per bf16 logit, and that traffic is
+// the bound.
 //
-// In units of log2: a warp's largest logit m_w gives its reference point
-// r_w = m_w log2 e (rounded) and s_w = sum 2^(c log2 e - r_w) over its logits.
-// The pairs (m_w, s_w) of all warps of the cluster meet in every CTA's shared
-// memory behind one barrier; r = max r_w, S = sum s_w 2^(r_w - r),
-// nll = ln 2 (log2 S - (c_t log2 e - r)), softmax_v = 2^(c_v log2 e - r) / S.
-// The rounding of r is common to all of them and cancels.
+// A CTA's slice of a row lies in a ring of chunks, filled and emptied by bulk
+// copies that one thread issues. Pass 1 walks the chunks as they land, every
+// thread with its own running maximum m and sum s of 2^((c - m) log2 e); the
+// warps' pairs (m, s) meet in every CTA of the cluster. Pass 2 overwrites the
+// chunks by the gradient, each copied out as it is done and its place filled
+// with the next row's chunk.
+#include <algorithm>
 #include <cmath>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "ptx.cuh"
 
 namespace dspark {
 
 namespace {
 
-constexpr int kMaxThreads = 512;
-constexpr int kMaxCluster = 16;
+constexpr int kMaxThreads = 512;  // that compute; one warp more issues the copies
 constexpr int kMaxWarps = kMaxThreads / 32;
+constexpr int kMaxCluster = 16;
+constexpr int kMaxSlots = 8;
+constexpr int kRing = 222 * 1024;  // bytes, at most; the barriers and pairs take 4.4 KB more
+constexpr int kPerThread = 4;  // vectors of a chunk for each thread, at most
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.693147180559945309417f;
 
 // 2^x by the hardware approximation (relative error 2^-22; 0 below 2^-126).
 __device__ __forceinline__ float ex2(float x) {
@@ -38,11 +42,33 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// The factor from logits to the exponents' units for a row whose largest logit
-// is m. Where m log2 e could overflow, two logits that differ at all do so by
-// far more than any exponent, so a quarter of them serves as well (and stays
-// finite): equal logits have equal exponents, all others vanish.
-__device__ __forceinline__ float unit_for(float m) { return fabsf(m) > 0x1p126f ? 0.25f : kLog2e; }
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+// exp of x - m for a pair; minus_m holds -m twice.
+__device__ __forceinline__ float2 exp_pair(float2 x, float2 minus_m) {
+  const float2 t = mul2(add2(x, minus_m), make_float2(kLog2e, kLog2e));
+  return make_float2(ex2(t.x), ex2(t.y));
+}
+// The factor that brings a sum with reference m to reference top >= m. A
+// reference of -inf stands for an empty (or NaN) sum, kept as it is.
+__device__ __forceinline__ float rescaled(float s, float m, float top) {
+  return m == top || m == -INFINITY ? s : s * ex2((m - top) * kLog2e);
+}
 
 // A row counts when its target is not the ignored one, lies in the vocabulary
 // and its weight is not zero.
@@ -84,69 +110,47 @@ __device__ double inverse_total(const LossArgs& a, double* parts, bool report) {
   return s != 0.0 ? 1.0 / s : 0.0;
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t n;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
-  return n;
-}
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// Stores a pair at the same shared address of CTA `rank` of the cluster.
-__device__ __forceinline__ void store_remote(float2* p, uint32_t rank, float2 v) {
-  const uint32_t local = static_cast<uint32_t>(__cvta_generic_to_shared(p));
-  uint32_t remote;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
-  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(remote), "f"(v.x), "f"(v.y) : "memory");
-}
-
-// 16 bytes of a row.
+// 16 bytes of a row, as pairs of fp32.
 template <typename T>
 struct Vectors;
 template <>
 struct Vectors<float> {
   static constexpr int kE = 4;
   static constexpr uint32_t kFill = 0xff800000u;  // -inf
-  static __device__ __forceinline__ float get(const uint4& r, int e) {
-    return __uint_as_float(e == 0 ? r.x : e == 1 ? r.y : e == 2 ? r.z : r.w);
+  static __device__ __forceinline__ float2 pair(const uint4& r, int i) {
+    return i == 0 ? make_float2(__uint_as_float(r.x), __uint_as_float(r.y))
+                  : make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
   }
   static __device__ __forceinline__ float max_of(const uint4& r) {
-    return fmaxf(fmaxf(get(r, 0), get(r, 1)), fmaxf(get(r, 2), get(r, 3)));
+    const float2 a = pair(r, 0), b = pair(r, 1);
+    return fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y));
   }
-  static __device__ __forceinline__ uint4 pack(const float* g) {
-    return make_uint4(__float_as_uint(g[0]), __float_as_uint(g[1]), __float_as_uint(g[2]), __float_as_uint(g[3]));
+  static __device__ __forceinline__ uint4 pack(const float2* g) {
+    return make_uint4(__float_as_uint(g[0].x), __float_as_uint(g[0].y), __float_as_uint(g[1].x),
+                      __float_as_uint(g[1].y));
   }
 };
 template <>
 struct Vectors<__nv_bfloat16> {
   static constexpr int kE = 8;
   static constexpr uint32_t kFill = 0xff80ff80u;
-  static __device__ __forceinline__ uint32_t word(const uint4& r, int i) {
-    return i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w;
+  static __device__ __forceinline__ float2 pair(const uint4& r, int i) {
+    const uint32_t w = i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w;
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   }
-  static __device__ __forceinline__ float get(const uint4& r, int e) {
-    const uint32_t w = word(r, e >> 1);
-    return __uint_as_float((e & 1) ? (w & 0xffff0000u) : (w << 16));
-  }
-  static __device__ __forceinline__ __nv_bfloat162 pair(uint32_t w) {
+  static __device__ __forceinline__ __nv_bfloat162 both(uint32_t w) {
     return *reinterpret_cast<const __nv_bfloat162*>(&w);
   }
   static __device__ __forceinline__ float max_of(const uint4& r) {
-    const __nv_bfloat162 m = __hmax2(__hmax2(pair(r.x), pair(r.y)), __hmax2(pair(r.z), pair(r.w)));
+    const __nv_bfloat162 m = __hmax2(__hmax2(both(r.x), both(r.y)), __hmax2(both(r.z), both(r.w)));
     return fmaxf(__low2float(m), __high2float(m));
   }
-  static __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  static __device__ __forceinline__ uint32_t pack2(float2 x) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x.x, x.y);
     return *reinterpret_cast<const uint32_t*>(&v);
   }
-  static __device__ __forceinline__ uint4 pack(const float* g) {
-    return make_uint4(pack2(g[0], g[1]), pack2(g[2], g[3]), pack2(g[4], g[5]), pack2(g[6], g[7]));
+  static __device__ __forceinline__ uint4 pack(const float2* g) {
+    return make_uint4(pack2(g[0]), pack2(g[1]), pack2(g[2]), pack2(g[3]));
   }
 };
 
@@ -169,174 +173,299 @@ struct RowShape {
   __device__ __forceinline__ int edge(int k) const { return k < head ? k : k + vecs * Vectors<T>::kE; }
 };
 
-__device__ __forceinline__ float edge_value(const float* p) { return __ldcs(p); }
-__device__ __forceinline__ float edge_value(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+struct LossPlan {
+  int cluster;  // CTAs per row
+  int warps;    // that compute, per CTA
+  int slice;    // vectors of a row per CTA
+  int chunk;    // vectors per chunk, at most 32 kPerThread warps
+  int chunks;   // chunks per slice
+  int slots;    // chunks in the ring, at least `chunks`
+};
 
-// Rows for one cluster each, a persistent grid walking them; NV vectors of the
-// row in each thread's registers. While a row's gradient is written, each
-// vector's registers already load the next row's.
-// SAME: the gradient's rows start at the same offset from a 16-byte address as
-// the logits' (in place, or any vocabulary of whole vectors), so that a vector
-// read is a vector written; otherwise gradients are written one by one.
-template <typename T, int NV, bool SAME>
-__global__ void __launch_bounds__(kMaxThreads, 2) loss_rows_kernel(LossArgs a) {
-  constexpr int kE = Vectors<T>::kE;
-  __shared__ double sums[kMaxWarps];
-  __shared__ float2 parts[2][kMaxCluster * kMaxWarps];
-  const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t ranks = cluster_size(), rank = cluster_rank();
-  const int64_t step = gridDim.x / ranks;
-  const int vocab = (int)a.vocab, threads = (int)blockDim.x;
-  const int j0 = (int)rank * threads * NV + (int)threadIdx.x;  // this thread's vectors: j0 + n threads
-  const T* logits = static_cast<const T*>(a.logits);
-  T* grads = static_cast<T*>(a.grad);
+struct RowBarriers {
+  uint64_t full[kMaxSlots];  // a chunk has landed
+  uint64_t done[kMaxSlots];  // every warp has left a chunk
+  uint64_t met[2];           // a row's pairs are here
+};
 
-  uint4 raw[NV];
-  float edge = -INFINITY, xt = 0.0f;  // this thread's edge element; the target's logit (thread 0)
-  auto load = [&](int64_t row, int n) {
-    const T* c = logits + row * vocab;
-    const RowShape<T> shape(c, vocab);
-    const int j = j0 + n * threads;
-    raw[n] = j < shape.vecs ? __ldcs(reinterpret_cast<const uint4*>(c + shape.head) + j)
-                            : make_uint4(Vectors<T>::kFill, Vectors<T>::kFill, Vectors<T>::kFill, Vectors<T>::kFill);
-  };
-  auto load_singles = [&](int64_t row, int64_t t) {
-    const T* c = logits + row * vocab;
-    const RowShape<T> shape(c, vocab);
-    edge = -INFINITY;
-    if (rank == 0) {
-      if ((int)threadIdx.x < shape.edges) edge = edge_value(c + shape.edge((int)threadIdx.x));
-      if (threadIdx.x == 0) xt = edge_value(c + t);
-    }
-  };
-
-  int64_t i = blockIdx.x / ranks;
-  int64_t t = 0;
-  float w = 0.0f;
-  bool live = i < a.rows && live_row(a, i, &t, &w);
-  if (live) {
-#pragma unroll
-    for (int n = 0; n < NV; ++n) load(i, n);
-    load_singles(i, t);
-  }
-  const double inv_n = inverse_total(a, sums, false);
-  if (ranks > 1) cluster_barrier();  // every CTA's shared memory is there
-
-  int parity = 0;
-  while (i < a.rows) {
-    const int64_t next = i + step;
-    int64_t next_t = 0;
-    float next_w = 0.0f;
-    const bool next_live = next < a.rows && live_row(a, next, &next_t, &next_w);
-    const RowShape<T> shape(logits + i * vocab, vocab);
-    T* g = grads + i * vocab;
-    if (!live) {
-      if (rank == 0 && threadIdx.x == 0) a.row_losses[i] = 0.0f;
-      if (rank == 0 && grads && (int)threadIdx.x < shape.edges) g[shape.edge((int)threadIdx.x)] = from_f32<T>(0.0f);
-#pragma unroll
-      for (int n = 0; n < NV; ++n) {
-        const int j = j0 + n * threads;
-        if (grads && j < shape.vecs) {
-          if (SAME)
-            __stcs(reinterpret_cast<uint4*>(g + shape.head) + j, make_uint4(0u, 0u, 0u, 0u));
-          else
-            for (int e = 0; e < kE; ++e) g[shape.head + j * kE + e] = from_f32<T>(0.0f);
-        }
-        if (next_live) load(next, n);
-      }
-      if (next_live) load_singles(next, next_t);
-    } else {
-      float m = edge;
-#pragma unroll
-      for (int n = 0; n < NV; ++n) m = fmaxf(m, Vectors<T>::max_of(raw[n]));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      // A warp of -inf alone (or NaN) takes 0 as its reference and sums zeros (or NaN).
-      float unit = m == -INFINITY ? kLog2e : unit_for(m);
-      float ref = m == -INFINITY ? 0.0f : m * unit;
-      float s = ex2(fmaf(edge, unit, -ref));
-#pragma unroll
-      for (int n = 0; n < NV; ++n)
-#pragma unroll
-        for (int e = 0; e < kE; ++e) s += ex2(fmaf(Vectors<T>::get(raw[n], e), unit, -ref));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      // The warp's pair into every CTA. The buffer written two rows ago was
-      // read before the last barrier.
-      if (lane < (int)ranks)
-        store_remote(&parts[parity][rank * warps + warp], (uint32_t)lane, make_float2(m, s));
-      if (ranks > 1)
-        cluster_barrier();
-      else
-        __syncthreads();
-      const int pairs = (int)ranks * warps;
-      m = -INFINITY;
-      for (int k = lane; k < pairs; k += 32) m = fmaxf(m, parts[parity][k].x);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      unit = unit_for(m);
-      ref = m * unit;
-      float sum = 0.0f;
-      for (int k = lane; k < pairs; k += 32) {
-        const float2 q = parts[parity][k];
-        // A warp in other units lies infinitely far below.
-        if (q.x == -INFINITY)
-          sum += q.y;
-        else if (unit_for(q.x) == unit)
-          sum += q.y * ex2(q.x * unit - ref);
-        else
-          sum += q.y * 0.0f;  // NaN stays
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      parity ^= 1;
-      if (isinf(m)) sum = NAN;  // +inf somewhere, or -inf everywhere
-      const float scale = (float)((double)w * inv_n);
-      const float factor = scale / sum;
-      if (rank == 0 && threadIdx.x == 0)  // in plain units where the exponents' would overflow
-        a.row_losses[i] = unit == kLog2e && fabsf(xt) <= 0x1p126f ? kLn2 * (log2f(sum) - fmaf(xt, unit, -ref)) : logf(sum) + (m - xt);
-      // The target's place among the vectors (negative or past them: an edge).
-      const int at = (int)t - shape.head;
-      const int tj = at >= 0 ? at / kE : -1, te = at % kE;
-      if (grads && rank == 0 && (int)threadIdx.x < shape.edges) {
-        const int v = shape.edge((int)threadIdx.x);
-        const float p = ex2(fmaf(edge, unit, -ref)) * factor;
-        g[v] = from_f32<T>(v == (int)t ? p - scale : p);
-      }
-#pragma unroll
-      for (int n = 0; n < NV; ++n) {
-        const int j = j0 + n * threads;
-        if (grads && j < shape.vecs) {
-          float p[kE];
-#pragma unroll
-          for (int e = 0; e < kE; ++e) p[e] = ex2(fmaf(Vectors<T>::get(raw[n], e), unit, -ref)) * factor;
-          if (j == tj) {
-#pragma unroll
-            for (int e = 0; e < kE; ++e)
-              if (e == te) p[e] -= scale;
-          }
-          if (SAME) {
-            __stcs(reinterpret_cast<uint4*>(g + shape.head) + j, Vectors<T>::pack(p));
-          } else {
-#pragma unroll
-            for (int e = 0; e < kE; ++e) g[shape.head + j * kE + e] = from_f32<T>(p[e]);
-          }
-        }
-        if (next_live) load(next, n);
-      }
-      if (next_live) load_singles(next, next_t);
-    }
-    i = next;
-    t = next_t;
-    w = next_w;
-    live = next_live;
-  }
+// Chunk c of a slice of `count` vectors: the vectors in it.
+__device__ __forceinline__ int chunk_vectors(const LossPlan& p, int count, int c) {
+  return max(0, min(p.chunk, count - c * p.chunk));
+}
+// The vectors of a row that lie in CTA `rank`'s slice.
+__device__ __forceinline__ int slice_vectors(const LossPlan& p, int vecs, int rank) {
+  return max(0, min(p.slice, vecs - rank * p.slice));
 }
 
-// Rows longer than a cluster's registers: one CTA per row reads it twice.
+// SAME: the gradient's rows start at the same offset from a 16-byte address as
+// the logits' (in place, or any vocabulary of whole vectors), so that a chunk
+// is copied out as it was copied in; otherwise gradients are written one by one.
+template <typename T, bool SAME>
+__global__ void __launch_bounds__(kMaxThreads + 32, 1) loss_rows_kernel(LossArgs a, LossPlan p) {
+  constexpr int kE = Vectors<T>::kE;
+  extern __shared__ __align__(128) uint4 ring[];
+  __shared__ RowBarriers bars;
+  __shared__ float2 pairs[2][kMaxCluster * kMaxWarps];
+  __shared__ double sums[kMaxWarps + 1];
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = (int)threadIdx.x;
+  const int ranks = p.cluster, rank = (int)cluster_rank(), warps = p.warps, threads = warps * 32;
+  const int64_t step = gridDim.x / ranks, first = blockIdx.x / ranks;
+  const int vocab = (int)a.vocab;
+  const T* logits = static_cast<const T*>(a.logits);
+  T* grads = static_cast<T*>(a.grad);
+  const WaitCtl ctl{&abort_flag, a.status, a.wait_limit_ns};
+  // The next live row at or after i.
+  auto seek = [&](int64_t i, int64_t* t, float* w) {
+    while (i < a.rows && !live_row(a, i, t, w)) i += step;
+    return i;
+  };
+
+  if (tid == 0) {
+    abort_flag = 0;
+    for (int k = 0; k < p.slots; ++k) {
+      mbar_init(&bars.full[k], 1);
+      mbar_init(&bars.done[k], (uint32_t)warps);
+    }
+    mbar_init(&bars.met[0], (uint32_t)(ranks * warps));
+    mbar_init(&bars.met[1], (uint32_t)(ranks * warps));
+    fence_barrier_init();
+  }
+  const double inv_n = inverse_total(a, sums, false);
+  __syncthreads();
+  if (ranks > 1) cluster_barrier();  // every CTA's barriers are there
+
+  if (warp == warps) {
+    if (lane == 0) {
+      // The copies: chunk q goes to slot q % slots once the chunk that was
+      // there has been copied out.
+      int64_t t;
+      float w;
+      int64_t out_row = first, in_row = first;
+      int out_c = 0, slot = 0, out_slot = 0;
+      uint32_t out_phase = 0;
+      int64_t in_flight = 0;  // chunks loaded and not yet copied out
+      out_row = seek(out_row, &t, &w);
+      auto copy_out = [&]() {
+        if (!mbar_wait(&bars.done[out_slot], out_phase, ctl)) return false;
+        if (SAME && grads) {
+          const RowShape<T> shape(logits + out_row * vocab, vocab);
+          const int n = chunk_vectors(p, slice_vectors(p, shape.vecs, rank), out_c);
+          if (n > 0) {
+            T* to = grads + out_row * vocab + shape.head + ((int64_t)rank * p.slice + out_c * p.chunk) * kE;
+            bulk_store(to, ring + (size_t)out_slot * p.chunk, (uint32_t)n * 16u);
+            bulk_commit_group();
+            bulk_wait_group_read<0>();
+          }
+        }
+        if (++out_slot == p.slots) {
+          out_slot = 0;
+          out_phase ^= 1u;
+        }
+        if (++out_c == p.chunks) {
+          out_c = 0;
+          out_row = seek(out_row + step, &t, &w);
+        }
+        --in_flight;
+        return true;
+      };
+      bool ok = true;
+      for (in_row = seek(in_row, &t, &w); ok && in_row < a.rows; in_row = seek(in_row + step, &t, &w)) {
+        const RowShape<T> shape(logits + in_row * vocab, vocab);
+        const int count = slice_vectors(p, shape.vecs, rank);
+        const T* from = logits + in_row * vocab + shape.head + (int64_t)rank * p.slice * kE;
+        for (int c = 0; c < p.chunks; ++c) {
+          if (in_flight == p.slots && !(ok = copy_out())) break;
+          const int n = chunk_vectors(p, count, c);
+          if (n > 0) {
+            mbar_arrive_expect_tx(&bars.full[slot], (uint32_t)n * 16u);
+            bulk_load(ring + (size_t)slot * p.chunk, from + (int64_t)c * p.chunk * kE, (uint32_t)n * 16u,
+                      &bars.full[slot]);
+          } else {
+            mbar_arrive(&bars.full[slot]);
+          }
+          ++in_flight;
+          if (++slot == p.slots) slot = 0;
+        }
+      }
+      while (ok && in_flight > 0) ok = copy_out();
+      bulk_wait_group<0>();
+      // After a wait that ran out, copies still under way end before the CTA does.
+      if (!ok) {
+        const uint64_t t0 = globaltimer_ns();
+        for (int k = 0; k < p.slots && in_flight > 0; ++k)
+          for (uint32_t phase = 0; phase < 2; ++phase)
+            while (!mbar_try_wait(&bars.full[k], phase) && globaltimer_ns() - t0 < a.wait_limit_ns) {
+            }
+      }
+    }
+    __syncwarp();
+  } else {
+    int slot1 = 0, slot2 = 0, parity = 0;  // of pass 1 and pass 2 in the ring; of the pairs' buffer
+    uint32_t phase1 = 0, met_phase = 0;
+    int64_t i = first;
+    int64_t t = 0;
+    float w = 0.0f;
+    float edge = -INFINITY, xt = 0.0f;  // this thread's edge element; the target's logit (thread 0)
+    auto load_singles = [&](int64_t row, int64_t target) {
+      const T* c = logits + row * vocab;
+      const RowShape<T> shape(c, vocab);
+      edge = -INFINITY;
+      if (rank == 0) {
+        if (tid < shape.edges) edge = to_f32(c[shape.edge(tid)]);
+        if (tid == 0) xt = to_f32(c[target]);
+      }
+    };
+    bool live = i < a.rows && live_row(a, i, &t, &w);
+    if (live) load_singles(i, t);
+    while (i < a.rows) {
+      const int64_t next = i + step;
+      int64_t next_t = 0;
+      float next_w = 0.0f;
+      const bool next_live = next < a.rows && live_row(a, next, &next_t, &next_w);
+      const RowShape<T> shape(logits + i * vocab, vocab);
+      const int count = slice_vectors(p, shape.vecs, rank);
+      T* g = grads ? grads + i * vocab : nullptr;
+      if (!live) {
+        if (rank == 0 && tid == 0) a.row_losses[i] = 0.0f;
+        if (g) {
+          if (rank == 0 && tid < shape.edges) g[shape.edge(tid)] = from_f32<T>(0.0f);
+          T* to = g + shape.head + (int64_t)rank * p.slice * kE;
+          if (SAME) {
+            for (int j = tid; j < count; j += threads)
+              __stcs(reinterpret_cast<uint4*>(to) + j, make_uint4(0u, 0u, 0u, 0u));
+          } else {
+            for (int j = tid; j < count * kE; j += threads) to[j] = from_f32<T>(0.0f);
+          }
+        }
+        if (next_live) load_singles(next, next_t);
+      } else {
+        // Pass 1. A thread of -inf alone keeps m = -inf and sums zeros (or NaN).
+        float m = edge;
+        float s = edge == -INFINITY ? 0.0f : ex2((edge - edge) * kLog2e);
+        for (int c = 0; c < p.chunks; ++c) {
+          mbar_wait(&bars.full[slot1], phase1, ctl);
+          const int n = chunk_vectors(p, count, c);
+          const uint4* from = ring + (size_t)slot1 * p.chunk + tid;
+          uint4 raw[kPerThread];
+#pragma unroll
+          for (int k = 0; k < kPerThread; ++k) {
+            raw[k] = make_uint4(Vectors<T>::kFill, Vectors<T>::kFill, Vectors<T>::kFill, Vectors<T>::kFill);
+            if (tid + k * threads < n) raw[k] = from[k * threads];
+          }
+          float top = m;
+#pragma unroll
+          for (int k = 0; k < kPerThread; ++k) top = fmaxf(top, Vectors<T>::max_of(raw[k]));
+          s = rescaled(s, m, top);
+          m = top;
+          const float minus = top == -INFINITY ? 0.0f : -top;
+          float2 sum[2] = {make_float2(s, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+          for (int k = 0; k < kPerThread; ++k)
+#pragma unroll
+            for (int e = 0; e < kE / 2; ++e)
+              sum[e & 1] = add2(sum[e & 1], exp_pair(Vectors<T>::pair(raw[k], e), make_float2(minus, minus)));
+          s = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          if (++slot1 == p.slots) {
+            slot1 = 0;
+            phase1 ^= 1u;
+          }
+        }
+        float top = m;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        s = rescaled(s, m, top);
+        m = top;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        // The warp's pair to every CTA. The other of the two buffers may still
+        // be read; this one was left by all warps before they sent the pairs
+        // that ended the last row's wait.
+        if (ranks > 1) {
+          if (lane < ranks) {
+            store_remote(remote_u32(&pairs[parity][rank * warps + warp], (uint32_t)lane), m, s);
+            mbar_arrive_remote(remote_u32(&bars.met[parity], (uint32_t)lane));
+          }
+        } else if (lane == 0) {
+          pairs[parity][warp] = make_float2(m, s);
+          mbar_arrive(&bars.met[parity]);
+        }
+        __syncwarp();
+        const float row_xt = xt, row_edge = edge;
+        if (next_live) load_singles(next, next_t);
+        mbar_wait_cluster(&bars.met[parity], met_phase, ctl);
+        m = -INFINITY;
+        for (int k = lane; k < ranks * warps; k += 32) m = fmaxf(m, pairs[parity][k].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        s = 0.0f;
+        for (int k = lane; k < ranks * warps; k += 32) s += rescaled(pairs[parity][k].y, pairs[parity][k].x, m);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        parity ^= 1;
+        if (parity == 0) met_phase ^= 1u;
+        if (isinf(m)) s = NAN;  // +inf somewhere, or -inf everywhere
+        const float scale = (float)((double)w * inv_n), factor = scale / s;
+        if (rank == 0 && tid == 0) a.row_losses[i] = logf(s) + (m - row_xt);
+        if (g && rank == 0 && tid < shape.edges) {
+          const int v = shape.edge(tid);
+          const float e = ex2((row_edge - m) * kLog2e) * factor;
+          g[v] = from_f32<T>(v == (int)t ? e - scale : e);
+        }
+        // Pass 2. The target's place in this slice, counted in vectors.
+        const int at = (int)t - shape.head;
+        const int target = at >= 0 ? at / kE - rank * p.slice : -1, te = at % kE;
+        T* to = g + shape.head + (int64_t)rank * p.slice * kE;
+        for (int c = 0; c < p.chunks; ++c) {
+          const int n = g ? chunk_vectors(p, count, c) : 0;
+          uint4* place = ring + (size_t)slot2 * p.chunk + tid;
+#pragma unroll
+          for (int k = 0; k < kPerThread; ++k) {
+            const int j = tid + k * threads;
+            if (j < n) {
+              const uint4 raw = place[k * threads];
+              float2 x[kE / 2];
+#pragma unroll
+              for (int e = 0; e < kE / 2; ++e)
+                x[e] = mul2(exp_pair(Vectors<T>::pair(raw, e), make_float2(-m, -m)), make_float2(factor, factor));
+              if (c * p.chunk + j == target) {
+#pragma unroll
+                for (int e = 0; e < kE / 2; ++e) {
+                  if (2 * e == te) x[e].x -= scale;
+                  if (2 * e + 1 == te) x[e].y -= scale;
+                }
+              }
+              if (SAME) {
+                place[k * threads] = Vectors<T>::pack(x);
+              } else {
+#pragma unroll
+                for (int e = 0; e < kE / 2; ++e) {
+                  to[((int64_t)c * p.chunk + j) * kE + 2 * e] = from_f32<T>(x[e].x);
+                  to[((int64_t)c * p.chunk + j) * kE + 2 * e + 1] = from_f32<T>(x[e].y);
+                }
+              }
+            }
+          }
+          if (SAME) fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.done[slot2]);
+          if (++slot2 == p.slots) slot2 = 0;
+        }
+      }
+      i = next;
+      t = next_t;
+      w = next_w;
+      live = next_live;
+    }
+    __syncwarp();
+  }
+  if (ranks > 1) cluster_barrier();  // no CTA leaves while others may still send to it
+}
+
+// Rows longer than a cluster's shared memory: one CTA per row reads it twice.
 template <typename T>
 __global__ void __launch_bounds__(kMaxThreads) loss_long_rows_kernel(LossArgs a) {
-  __shared__ double sums[kMaxWarps];
+  __shared__ double sums[kMaxWarps + 1];
   __shared__ float2 parts[kMaxWarps];
   const double inv_n = inverse_total(a, sums, false);
   for (int64_t i = blockIdx.x; i < a.rows; i += gridDim.x) {
@@ -387,7 +516,7 @@ __global__ void __launch_bounds__(kMaxThreads) loss_long_rows_kernel(LossArgs a)
 
 // loss = sum_i w_i nll_i / N over the live rows, and the status of the targets.
 __global__ void __launch_bounds__(kMaxThreads) loss_sum_kernel(LossArgs a) {
-  __shared__ double sums[kMaxWarps];
+  __shared__ double sums[kMaxWarps + 1];
   const double inv_n = inverse_total(a, sums, true);
   double s = 0.0;
   for (int64_t i = threadIdx.x; i < a.rows; i += blockDim.x) {
@@ -399,73 +528,68 @@ __global__ void __launch_bounds__(kMaxThreads) loss_sum_kernel(LossArgs a) {
   if (threadIdx.x == 0) *a.loss = (float)(s * inv_n);
 }
 
-struct LossPlan {
-  int cluster, threads, vectors;  // vectors per thread
-};
-
-// The cluster that holds a row of `vecs` vectors, or cluster 0 where none does.
+// The cluster and ring for a row of `vecs` vectors, or cluster 0 where none
+// holds it.
 LossPlan plan_loss(int64_t rows, int64_t vecs, int num_sms) {
-  LossPlan p{1, 0, 8};
-  while (p.cluster <= kMaxCluster && (int64_t)p.cluster * kMaxThreads * 8 < vecs) p.cluster *= 2;
-  if (p.cluster > kMaxCluster) return LossPlan{0, 0, 0};
-  // Few rows: more, smaller CTAs per row.
-  while (rows * p.cluster < num_sms && p.cluster < 8 && vecs >= (int64_t)p.cluster * 2 * 128 * 2) p.cluster *= 2;
-  const int64_t per_cta = (vecs + p.cluster - 1) / p.cluster;
-  while (p.vectors > 1 && per_cta < (int64_t)p.vectors * 128) p.vectors /= 2;
-  const int64_t threads = (per_cta + p.vectors - 1) / p.vectors;
-  p.threads = (int)(threads > 0 ? (threads + 31) / 32 * 32 : 32);
+  constexpr int64_t kMaxSlice = 9728;  // vectors; 152 KB, so that the ring has room beyond a slice
+  constexpr int64_t kRingBytes = kRing;
+  int64_t cluster = 1;
+  while (cluster <= kMaxCluster && cluster * kMaxSlice < vecs) cluster *= 2;
+  LossPlan p{};
+  if (cluster > kMaxCluster) return p;
+  // Few rows: more CTAs for each.
+  while (rows * cluster * 2 <= num_sms && cluster < 8 && vecs >= cluster * 2 * 512) cluster *= 2;
+  const int64_t slice = std::max<int64_t>(1, (vecs + cluster - 1) / cluster);
+  p.cluster = (int)cluster;
+  p.slice = (int)slice;
+  p.warps = (int)std::min<int64_t>(kMaxWarps, std::max<int64_t>(2, (slice + 63) / 64));
+  const int64_t most = (int64_t)p.warps * 32 * kPerThread;
+  p.chunks = (int)((slice + most - 1) / most);
+  p.chunk = (int)((slice + p.chunks - 1) / p.chunks);
+  int64_t slots = std::min<int64_t>(kMaxSlots, kRingBytes / ((int64_t)p.chunk * 16));
+  if (slots > p.chunks + 3) slots = p.chunks + 3;
+  p.slots = (int)slots;
   return p;
 }
 
-template <typename T, int NV, bool SAME>
+template <typename T, bool SAME>
 cudaError_t launch_rows(const LossArgs& a, const LossPlan& p, int num_sms, cudaStream_t s) {
-  auto kernel = loss_rows_kernel<T, NV, SAME>;
+  auto kernel = loss_rows_kernel<T, SAME>;
   cudaLaunchConfig_t cfg{};
-  cfg.blockDim = dim3((unsigned)p.threads);
+  cfg.blockDim = dim3((unsigned)(p.warps * 32 + 32));
+  cfg.dynamicSmemBytes = (size_t)p.slots * p.chunk * 16;
   cfg.stream = s;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim = {(unsigned)p.cluster, 1, 1};
   cfg.attrs = &attr;
   cfg.numAttrs = p.cluster > 1 ? 1 : 0;
-  if (p.cluster > 8) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-  }
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
+  if (e == cudaSuccess && p.cluster > 8)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
   // As many clusters as run at once: a persistent grid larger than that would
   // leave its last clusters, and their rows, to a second wave.
   cfg.gridDim = dim3((unsigned)p.cluster);
   int clusters = 0;
-  cudaError_t e;
   if (p.cluster > 1) {
     e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
   } else {
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&clusters, kernel, p.threads, 0);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&clusters, kernel, (int)cfg.blockDim.x, cfg.dynamicSmemBytes);
     clusters *= num_sms;
   }
   if (e != cudaSuccess) return e;
   if (clusters < 1) clusters = 1;
   if (clusters > a.rows) clusters = (int)a.rows;
   cfg.gridDim = dim3((unsigned)(clusters * p.cluster));
-  e = cudaLaunchKernelEx(&cfg, kernel, a);
+  e = cudaLaunchKernelEx(&cfg, kernel, a, p);
   note_launch();
   return e;
 }
 
-template <typename T, bool SAME>
-cudaError_t launch_vectors(const LossArgs& a, const LossPlan& p, int num_sms, cudaStream_t s) {
-  switch (p.vectors) {
-    case 1: return launch_rows<T, 1, SAME>(a, p, num_sms, s);
-    case 2: return launch_rows<T, 2, SAME>(a, p, num_sms, s);
-    case 4: return launch_rows<T, 4, SAME>(a, p, num_sms, s);
-    default: return launch_rows<T, 8, SAME>(a, p, num_sms, s);
-  }
-}
-
 template <typename T>
 cudaError_t launch_typed(const LossArgs& a, int num_sms, cudaStream_t s) {
-  constexpr int kE = Vectors<T>::kE;
-  const LossPlan p = plan_loss(a.rows, a.vocab / kE, num_sms);
+  const LossPlan p = plan_loss(a.rows, a.vocab / Vectors<T>::kE, num_sms);
   if (p.cluster == 0) {
     const int64_t grid = a.rows < 2ll * num_sms ? a.rows : 2ll * num_sms;
     loss_long_rows_kernel<T><<<(unsigned)grid, kMaxThreads, 0, s>>>(a);
@@ -473,7 +597,7 @@ cudaError_t launch_typed(const LossArgs& a, int num_sms, cudaStream_t s) {
     return cudaGetLastError();
   }
   const bool same = !a.grad || (reinterpret_cast<uintptr_t>(a.logits) - reinterpret_cast<uintptr_t>(a.grad)) % 16 == 0;
-  return same ? launch_vectors<T, true>(a, p, num_sms, s) : launch_vectors<T, false>(a, p, num_sms, s);
+  return same ? launch_rows<T, true>(a, p, num_sms, s) : launch_rows<T, false>(a, p, num_sms, s);
 }
 
 }  // namespace

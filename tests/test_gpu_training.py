@@ -72,7 +72,7 @@ def _check_loss(got, x, t, w, mean=True, ignore=-100):
 
 
 LOSS_SHAPES = [(1, 1), (3, 2), (10, 1024), (5, 7), (2, 4095), (4, 4096), (3, 4097), (7, 32003), (1, 40001), (2, 65536),
-               (3, 70001), (3, 129280), (2, 151936), (1, 262147), (1, 600001), (700, 33), (2100, 5)]
+               (3, 70001), (3, 129280), (2, 151936), (1, 262147), (1, 600001), (2, 1300001), (150, 100003), (700, 33), (2100, 5)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
