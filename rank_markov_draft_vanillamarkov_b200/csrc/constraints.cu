@@ -13,11 +13,13 @@
 // Almost every logit only passes through, so the bound is the copy: 4 bytes
 // per bf16 logit and an eighth of a byte of mask. A CTA takes one stretch of
 // the vocabulary of one sequence and walks that sequence's rows over it. It
-// first builds the stretch's state in shared memory: a word per id (prompt
-// bit and count), the last bias entry of each id, and one bit per id that has
-// either. Rows then go by 16-byte vectors: a mask byte and a byte of those
-// bits decide for eight logits at once. The history is read once per cluster:
-// its CTAs share the reading and send each id to the CTA that owns it.
+// first builds the stretch's state in shared memory from the whole history
+// (which comes from L2 for all but the first): a count and a prompt bit per
+// id, the last bias entry of each id, and a list of the ids that have any of
+// these or are drafted. Rows then go by 16-byte vectors, masked and copied,
+// eight rows at a time, and the few listed logits of all eight are worked out
+// afterwards, one thread for each; within the copy they would cost every warp
+// the whole arithmetic for a lane or two.
 #include <algorithm>
 #include <cmath>
 
@@ -29,19 +31,52 @@ namespace dspark {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kBatch = 4;                     // vectors in flight per thread
-constexpr int kAhead = 4;                     // history ids in flight per thread
-constexpr int kMinStretch = 1024;             // ids
-constexpr int kMaxStretch = 8192;
-constexpr uint32_t kPromptBit = 0x80000000u;  // count word: seen in the prompt; low bits: generated occurrences
+constexpr int kMaxThreads = 512;
+constexpr int kInFlight = 4;       // vectors under way per thread
+constexpr int kRows = 8;           // rows copied before their listed logits are worked out
+constexpr int kListed = 4;         // listed logits in flight per thread
+constexpr int kAhead = 8;          // history ids in flight per thread
+constexpr int kMinStretch = 512;   // ids
+constexpr int kMaxStretch = 32256;
+constexpr int kSmem = 222 * 1024;  // dynamic shared memory of a CTA, at most
 
 struct ConstrainPlan {
-  int stretch;    // ids per CTA, a power of two from kMinStretch
-  int shift;      // its logarithm
-  int stretches;  // per sequence, rounded up to whole clusters
-  int cluster;    // CTAs that share the reading of a history
+  int stretch;    // ids per CTA, a multiple of kMinStretch
+  int stretches;  // per sequence
+  int threads;    // per CTA
   int has_bias;
+};
+
+// Bytes of state per kMinStretch ids: counts and bias entries of W bytes each,
+// the list, prompt and touched bits.
+constexpr int64_t state_bytes(int64_t stretch, int width, bool has_bias) {
+  return stretch * (width * (has_bias ? 2 : 1) + 2) + stretch / 8 * 2;
+}
+
+// An array of counts, or of the last entry of each id, in shared memory.
+// 16-bit elements share the atomics of their 32-bit word.
+template <typename C>
+struct Cells;
+template <>
+struct Cells<uint32_t> {
+  static __device__ __forceinline__ void add(uint32_t* a, int l) { atomicAdd(&a[l], 1u); }
+  static __device__ __forceinline__ void keep_max(uint32_t* a, int l, uint32_t x) { atomicMax(&a[l], x); }
+};
+template <>
+struct Cells<uint16_t> {
+  static __device__ __forceinline__ void add(uint16_t* a, int l) {
+    atomicAdd(reinterpret_cast<uint32_t*>(a) + (l >> 1), (l & 1) ? 0x10000u : 1u);
+  }
+  static __device__ __forceinline__ void keep_max(uint16_t* a, int l, uint32_t x) {
+    uint32_t* word = reinterpret_cast<uint32_t*>(a) + (l >> 1);
+    const int shift = (l & 1) * 16;
+    uint32_t seen = *reinterpret_cast<volatile uint32_t*>(word);
+    while (((seen >> shift) & 0xffffu) < x) {  // ends: the half only grows, and by whoever wins
+      const uint32_t was = atomicCAS(word, seen, (seen & ~(0xffffu << shift)) | (x << shift));
+      if (was == seen) break;
+      seen = was;
+    }
+  }
 };
 
 // The bits of a bit string from bit `at` on. Where `at` is a multiple of 8 the
@@ -53,6 +88,7 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t* words, int at, int l
   const uint32_t lo = words[w], hi = w < last_word ? words[w + 1] : 0u;
   return __funnelshift_r(lo, hi, at & 31);
 }
+__device__ __forceinline__ bool bit(const uint32_t* words, int at) { return (words[at >> 5] >> (at & 31)) & 1u; }
 
 // Bits 0..3 of n as all-ones or zero halves of two words: element 2i in the
 // low half of word i. The product spreads the bits to the signs of four bytes
@@ -124,48 +160,43 @@ struct Vec<__nv_bfloat16> {
   }
 };
 
-// One logit with its state.
-struct Penalty {
-  float repetition, frequency, presence;
-  __device__ __forceinline__ float apply(float x, uint32_t count) const {
-    const uint32_t times = count & ~kPromptBit;
-    if (count) x = x > 0.0f ? __fdiv_rn(x, repetition) : __fmul_rn(x, repetition);
-    if (times) x = __fsub_rn(__fsub_rn(x, __fmul_rn(frequency, (float)times)), presence);
-    return x;
-  }
-};
-
 __device__ __forceinline__ unsigned long long max_key(unsigned long long a, unsigned long long b) {
   return a > b ? a : b;
 }
 
-template <typename T, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads, 3) constrain_kernel(ConstrainArgs a, ConstrainPlan p) {
+// C: uint16_t where no count nor bias entry passes 65535, else uint32_t.
+// ALIGNED: every row starts at a 16-byte address, in and out.
+template <typename T, typename C, bool ALIGNED>
+__global__ void __launch_bounds__(kMaxThreads, 2) constrain_kernel(ConstrainArgs a, ConstrainPlan p) {
   constexpr int kE = Vec<T>::kE;
   extern __shared__ __align__(16) uint32_t smem[];
-  __shared__ unsigned long long warp_best[2][kThreads / 32];
-  const int tid = (int)threadIdx.x, lane = tid & 31;
+  __shared__ int drafted[kRows];  // local ids (-1: elsewhere) of the tokens drafted after each of the rows
+  __shared__ unsigned long long warp_key[kRows][kMaxThreads / 32], listed_key[kRows];
+  __shared__ int listed_count;
+  const int tid = (int)threadIdx.x, lane = tid & 31, threads = (int)blockDim.x;
   const int64_t b = blockIdx.x / p.stretches;
   const int stretch = (int)(blockIdx.x % p.stretches);
-  const int64_t c0 = (int64_t)stretch * p.stretch;
-  const int n = (int)max((int64_t)0, min((int64_t)p.stretch, a.vocab - c0));  // none in a cluster's last CTAs, perhaps
-  const int rank = p.cluster > 1 ? (int)cluster_rank() : 0;
-  uint32_t* touched = smem;                     // stretch / 32 words
-  uint32_t* count = touched + p.stretch / 32;   // stretch words
-  uint32_t* slot = count + p.stretch;           // stretch words where there are biases
-
-  const int64_t rows = a.block;
+  const int64_t c0 = (int64_t)stretch * p.stretch, rows = a.block;
+  const int n = (int)min((int64_t)p.stretch, a.vocab - c0);
+  const int words = p.stretch / 32, mask_last = (n + 31) / 32 - 1;
+  uint32_t* touched = smem;
+  uint32_t* in_prompt = touched + words;
+  C* count = reinterpret_cast<C*>(in_prompt + words);
+  C* slot = count + p.stretch;  // where there are biases
+  uint16_t* list = reinterpret_cast<uint16_t*>(slot + (p.has_bias ? p.stretch : 0));
+  auto score = [&](float y, int64_t k, int l) {
+    const uint32_t v = (uint32_t)(c0 + l);
+    return pack_key(y / a.temperature + noise_for(a.seed, (uint32_t)b, (uint32_t)(a.draft_first + k), v), v);
+  };
 
   // A row's place: elements before the first 16-byte address, vectors, and
-  // what is left. Loads run one batch of vectors ahead, so that the first is
-  // under way while the state is built.
+  // what is left.
   struct Row {
     const T* in;
     T* out;
     const uint32_t* mask;
     int head, vecs;
   };
-  const int mask_last = (n + 31) / 32 - 1;
   auto row_at = [&](int64_t k) {
     Row r;
     r.in = static_cast<const T*>(a.in) + b * a.in_batch + k * a.in_row + c0;
@@ -180,191 +211,260 @@ __global__ void __launch_bounds__(kThreads, 3) constrain_kernel(ConstrainArgs a,
     r.vecs = (n - r.head) / kE;
     return r;
   };
-  uint4 ahead[kBatch];
-  uint32_t ahead_allowed[kBatch];
-  auto load = [&](const Row& r, int j0) {
-#pragma unroll
-    for (int q = 0; q < kBatch; ++q) {
-      const int j = j0 + tid + q * kThreads;
-      if (j < r.vecs) {
-        ahead[q] = __ldcs(reinterpret_cast<const uint4*>(r.in + r.head) + j);
-        ahead_allowed[q] = r.mask ? bits_at<ALIGNED>(r.mask, r.head + j * kE, mask_last) : ~0u;
+  // The thread's vectors of all rows in one stream: vector tid + q threads of
+  // row k, then the next q below `per_row`, then the next row. kInFlight of
+  // them are loaded ahead, the first while the state is built. A vector's mask
+  // words are shifted when used: a use here would wait for the load.
+  const int per_row = max(1, (n / kE + threads - 1) / threads);
+  struct Loaded {
+    uint4 raw;
+    uint32_t lo, hi;
+  };
+  Loaded ahead[kInFlight];
+  int64_t load_k = 0;
+  int load_q = 0;
+  Row load_row = row_at(0);
+  auto load = [&](Loaded& to) {
+    if (load_k >= rows) return;
+    const int j = tid + load_q * threads;
+    if (j < load_row.vecs) {
+      to.raw = __ldcs(reinterpret_cast<const uint4*>(load_row.in + load_row.head) + j);
+      if (load_row.mask) {
+        const int w = (load_row.head + j * kE) >> 5;
+        to.lo = load_row.mask[w];
+        if (!ALIGNED) to.hi = w < mask_last ? load_row.mask[w + 1] : 0u;
       }
     }
+    if (++load_q == per_row) {
+      load_q = 0;
+      if (++load_k < rows) load_row = row_at(load_k);
+    }
   };
-  Row row = row_at(0);
-  load(row, 0);
+#pragma unroll
+  for (int u = 0; u < kInFlight; ++u) load(ahead[u]);
 
-  for (int i = tid * 4; i < p.stretch; i += kThreads * 4) {
-    *reinterpret_cast<uint4*>(count + i) = make_uint4(0u, 0u, 0u, 0u);
-    if (p.has_bias) *reinterpret_cast<uint4*>(slot + i) = make_uint4(0u, 0u, 0u, 0u);
-  }
-  if (p.cluster > 1)
-    cluster_barrier();
-  else
-    __syncthreads();
-
-  bool bad = false;
+  // The state.
   const int64_t cap = a.history ? a.history_cap : 0;
   int64_t len = cap;
   if (a.history && a.history_lens) len = min(max(a.history_lens[b], (int64_t)0), cap);
   const int64_t prompt = a.prompt_lens ? min(max(a.prompt_lens[b], (int64_t)0), len) : 0;
-  const int64_t first = c0 - (int64_t)rank * p.stretch;  // the cluster's first id
-  auto note = [&](int64_t id, bool generated) {
-    const int64_t l = id - first;
-    if (l < 0 || l >= (int64_t)p.stretch * p.cluster || id >= a.vocab) return;
-    const int owner = (int)l >> p.shift, at = (int)l & (p.stretch - 1);
-    if (p.cluster == 1) {
-      if (generated)
-        atomicAdd(&count[at], 1u);
-      else
-        atomicOr(&count[at], kPromptBit);
-    } else {
-      const uint32_t where = remote_u32(&count[at], (uint32_t)owner);
-      if (generated)
-        asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(where), "r"(1u) : "memory");
-      else
-        asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(where), "r"(kPromptBit) : "memory");
+  if (tid == 0) listed_count = 0;
+  {
+    uint4* cells = reinterpret_cast<uint4*>(in_prompt);
+    const int vecs = (words * 4 + p.stretch * (int)sizeof(C) * (p.has_bias ? 2 : 1)) / 16;
+    for (int i = tid; i < vecs; i += threads) cells[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __syncthreads();
+  bool bad = false;
+  auto scan = [&](const int64_t* ids, int64_t from, int64_t to, bool padded, auto note) {
+    for (int64_t i = from + tid; i < to; i += (int64_t)threads * kAhead) {
+      int64_t id[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) id[u] = i + u * threads < to ? ids[i + u * threads] : c0 + n;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const uint64_t l = (uint64_t)(id[u] - c0);
+        if (l < (uint64_t)n) note((int)l, i + u * threads);
+        if (i + u * threads < to && (id[u] >= a.vocab || (id[u] < 0 && !padded))) bad = true;
+      }
     }
   };
-  const int64_t* history = a.history + b * a.history_stride;
-  const int64_t readers = (int64_t)kThreads * p.cluster;
-  for (int64_t i = (int64_t)rank * kThreads + tid; i < len; i += readers * kAhead) {
-    int64_t ids[kAhead];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) ids[u] = i + u * readers < len ? history[i + u * readers] : 0;
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (i + u * readers >= len) break;
-      if (ids[u] < 0 || ids[u] >= a.vocab) bad = true;
-      note(ids[u], i + u * readers >= prompt);
-    }
-  }
   const int64_t* draft = a.draft ? a.draft + b * a.draft_stride : nullptr;
-  for (int64_t i = (int64_t)rank * kThreads + tid; draft && i < a.draft_first; i += (int64_t)kThreads * p.cluster) {
-    const int64_t id = draft[i];
-    if (id >= a.vocab) bad = true;
-    if (id >= 0) note(id, true);
+  if (len > 0) {
+    const int64_t* history = a.history + b * a.history_stride;
+    scan(history, 0, prompt, false, [&](int l, int64_t) { atomicOr(&in_prompt[l >> 5], 1u << (l & 31)); });
+    scan(history, prompt, len, false, [&](int l, int64_t) { Cells<C>::add(count, l); });
   }
-  for (int64_t i = tid; i < a.bias_count; i += kThreads) {
-    const int64_t id = a.bias_ids[b * a.bias_stride + i];
-    if (id >= a.vocab) bad = true;
-    const int64_t l = id - c0;
-    if (l >= 0 && l < n) atomicMax(&slot[l], (uint32_t)i + 1u);
-  }
-  if (p.cluster > 1)
-    cluster_barrier();
-  else
-    __syncthreads();
-  for (int i = tid; i < p.stretch; i += kThreads) {  // whole warps: the stretch is a multiple of 32
-    const bool any = count[i] != 0u || (p.has_bias && slot[i] != 0u);
-    const uint32_t word = __ballot_sync(0xffffffffu, any);
-    if (lane == 0) touched[i >> 5] = word;
-  }
-  const Penalty penalty{a.repetition ? a.repetition[b] : a.repetition_value,
-                        a.frequency ? a.frequency[b] : a.frequency_value,
-                        a.presence ? a.presence[b] : a.presence_value};
-  const float* bias = a.bias_values + b * a.bias_stride;
-  auto one = [&](float x, int l) {  // the state of local id l applied to a logit
-    x = penalty.apply(x, count[l]);
-    if (p.has_bias) {
-      const uint32_t entry = slot[l];
-      if (entry) x = __fadd_rn(x, bias[entry - 1u]);
+  if (draft) scan(draft, 0, a.draft_first, true, [&](int l, int64_t) { Cells<C>::add(count, l); });
+  if (p.has_bias)
+    scan(a.bias_ids + b * a.bias_stride, 0, a.bias_count, true,
+         [&](int l, int64_t i) { Cells<C>::keep_max(slot, l, (uint32_t)i + 1u); });
+  __syncthreads();
+  {
+    // A word of bits for each 32 ids, 32 words a warp at a time; lane i keeps
+    // word i, and the warp takes its places in the list at once.
+    for (int w0 = (tid >> 5) * 32; w0 < words; w0 += threads) {
+      const int here = min(32, words - w0);
+      uint32_t word = 0u;
+      for (int i = 0; i < here; ++i) {
+        const int l = (w0 + i) * 32 + lane;
+        const uint32_t bits = __ballot_sync(0xffffffffu, count[l] != 0 || (p.has_bias && slot[l] != 0));
+        if (lane == i) word = bits;
+      }
+      if (lane < here) {
+        word |= in_prompt[w0 + lane];
+        touched[w0 + lane] = word;
+      }
+      const int mine = __popc(word);
+      int sum = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int before = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += before;
+      }
+      int base = 0;
+      if (lane == 31 && sum) base = atomicAdd(&listed_count, sum);
+      base = __shfl_sync(0xffffffffu, base, 31) + sum - mine;
+      for (; word; word &= word - 1u) list[base++] = (uint16_t)((w0 + lane) * 32 + __ffs((int)word) - 1);
     }
-    return x;
-  };
+  }
+  const float rho = a.repetition ? a.repetition[b] : a.repetition_value;
+  const float freq = a.frequency ? a.frequency[b] : a.frequency_value;
+  const float pres = a.presence ? a.presence[b] : a.presence_value;
+  const float* bias = a.bias_values + b * a.bias_stride;
   __syncthreads();
 
-  for (int64_t k = 0; k < rows; ++k) {
-    if (k > 0 && draft) {  // the token drafted before this row joins the history
-      if (tid == 0) {
-        const int64_t id = draft[a.draft_first + k - 1];
+  for (int64_t k0 = 0; k0 < rows; k0 += kRows) {
+    const int group = (int)min((int64_t)kRows, rows - k0);
+    // The last rows' drafted tokens join the counts. Those of these rows are
+    // laid out and listed, which changes nothing for rows before them.
+    if (draft && tid == 0) {
+      for (int q = 0; k0 > 0 && q < kRows; ++q)
+        if (drafted[q] >= 0) count[drafted[q]] += 1;
+      for (int q = 0; q < kRows; ++q) {
+        const int64_t id = k0 + q < rows - 1 ? draft[a.draft_first + k0 + q] : -1;
         if (id >= a.vocab) bad = true;
         const int64_t l = id - c0;
-        if (l >= 0 && l < n) {
-          count[l] += 1u;
+        const bool here = id >= 0 && l >= 0 && l < n;
+        drafted[q] = here ? (int)l : -1;
+        if (here && !bit(touched, (int)l)) {
           touched[l >> 5] |= 1u << (l & 31);
+          list[listed_count++] = (uint16_t)l;
         }
       }
-      __syncthreads();
     }
-    // Greedy: the largest so far and its local id. A row of -inf alone keeps
-    // the first threads' own ids, of which the lowest wins.
+    if (tid < kRows) listed_key[tid] = 0ull;
+    __syncthreads();
+
+    // The copy. Greedy keys: the largest value so far, the vector (and its
+    // first id) that holds it; a single element is a vector of its own. A row
+    // of -inf alone keeps the first threads' own ids, of which the lowest
+    // wins. Listed logits stand aside as -inf.
     float best = -INFINITY;
     int best_at = tid < n ? tid : -1;
+    uint4 best_vec = make_uint4(0u, 0u, 0u, 0u);
+    bool best_single = true;
     unsigned long long key = 0ull;
-    auto consider = [&](float y, int l) {
-      if (a.greedy) {
-        // Strictly larger, or a first NaN: ids rise, so equal values keep the lower one.
-        if (y > best || (y != y && best == best)) {
-          best = y;
-          best_at = l;
-        }
-      } else {
-        const uint32_t v = (uint32_t)(c0 + l);
-        key = max_key(key, pack_key(y / a.temperature + noise_for(a.seed, (uint32_t)b, (uint32_t)(a.draft_first + k), v), v));
-      }
-    };
-    auto scalar = [&](int l) {
-      float x = one(to_f32(row.in[l]), l);
-      if (row.mask && !((row.mask[l >> 5] >> (l & 31)) & 1u)) x = -INFINITY;
-      const T y = from_f32<T>(x);
+    // Strictly larger, or the first NaN: ids rise, so equal values keep the lower one.
+    auto better = [&](float y) { return y > best || (y != y && best == best); };
+    auto single = [&](const Row& row, int64_t k, int l) {
+      const T y = !row.mask || bit(row.mask, l) ? row.in[l] : from_f32<T>(-INFINITY);
       row.out[l] = y;
-      if (a.keys) consider(to_f32(y), l);
+      if (!a.keys || bit(touched, l)) return;
+      if (!a.greedy) {
+        key = max_key(key, score(to_f32(y), k, l));
+      } else if (better(to_f32(y))) {
+        best = to_f32(y);
+        best_at = l;
+        best_single = true;
+      }
     };
-    if (!ALIGNED)
-      for (int l = tid; l < row.head; l += kThreads) scalar(l);
-    uint4* to = reinterpret_cast<uint4*>(row.out + row.head);
-    const Row next = row_at(k + 1 < rows ? k + 1 : k);
-    int j0 = 0;
-    do {
-      uint4 raw[kBatch];
-      uint32_t allowed[kBatch];
+    int r = 0, q = 0;
+    Row row = row_at(k0);
+    while (r < group) {
 #pragma unroll
-      for (int q = 0; q < kBatch; ++q) {
-        raw[q] = ahead[q];
-        allowed[q] = ahead_allowed[q];
-      }
-      const int j1 = j0 + kThreads * kBatch;
-      if (j1 < row.vecs)
-        load(row, j1);
-      else if (k + 1 < rows)
-        load(next, 0);
+      for (int u = 0; u < kInFlight; ++u) {
+        if (r >= group) break;
+        if (!ALIGNED && q == 0)
+          for (int l = tid; l < row.head; l += threads) single(row, k0 + r, l);
+        const int j = tid + q * threads, l = row.head + j * kE;
+        if (j < row.vecs) {
+          uint4 raw = ahead[u].raw;
+          if (row.mask)
+            raw = Vec<T>::masked(raw, ALIGNED ? ahead[u].lo >> (l & 31)
+                                              : __funnelshift_r(ahead[u].lo, ahead[u].hi, l & 31));
+          __stcs(reinterpret_cast<uint4*>(row.out + row.head) + j, raw);
+          if (a.keys) {
+            raw = Vec<T>::masked(raw, ~bits_at<ALIGNED>(touched, l, words - 1));
+            if (a.greedy) {
+              const float top = Vec<T>::max_of(raw);
+              if (better(top)) {
+                best = top;
+                best_at = l;
+                best_vec = raw;
+                best_single = false;
+              }
+            } else {
 #pragma unroll
-      for (int q = 0; q < kBatch; ++q) {
-        const int j = j0 + tid + q * kThreads;
-        if (j >= row.vecs) break;
-        const int l = row.head + j * kE;
-        uint32_t t = bits_at<ALIGNED>(touched, l, p.stretch / 32 - 1) & ((1u << kE) - 1u) & allowed[q];
-        for (; t; t &= t - 1u) {
-          const int e = __ffs((int)t) - 1;
-          Vec<T>::set(raw[q], e, one(Vec<T>::get(raw[q], e), l + e));
+              for (int e = 0; e < kE; ++e) key = max_key(key, score(Vec<T>::get(raw, e), k0 + r, l + e));
+            }
+          }
         }
-        if (row.mask) raw[q] = Vec<T>::masked(raw[q], allowed[q]);
-        __stcs(to + j, raw[q]);
-        // Most vectors hold nothing larger than the thread's best.
-        if (a.keys && !(a.greedy && Vec<T>::max_of(raw[q]) <= best)) {
+        load(ahead[u]);
+        if (++q == per_row) {
+          for (int t = row.head + row.vecs * kE + tid; t < n; t += threads) single(row, k0 + r, t);
+          if (a.keys) {
+            if (a.greedy && best_at >= 0) {
+              if (!best_single) {
+                int first = kE;
 #pragma unroll
-          for (int e = 0; e < kE; ++e) consider(Vec<T>::get(raw[q], e), l + e);
+                for (int e = kE - 1; e >= 0; --e) {
+                  const float y = Vec<T>::get(best_vec, e);
+                  if (y == best || (y != y && best != best)) first = e;
+                }
+                best_at += first;
+              }
+              key = pack_key(best, (uint32_t)(c0 + best_at));
+            }
+            // The warp's largest key: the larger high word, then the larger low one.
+            const uint32_t high = __reduce_max_sync(0xffffffffu, (uint32_t)(key >> 32));
+            const uint32_t low = __reduce_max_sync(0xffffffffu, (uint32_t)(key >> 32) == high ? (uint32_t)key : 0u);
+            if (lane == 0) warp_key[r][tid >> 5] = ((unsigned long long)high << 32) | low;
+            best = -INFINITY;
+            best_at = tid < n ? tid : -1;
+            best_single = true;
+            key = 0ull;
+          }
+          q = 0;
+          if (++r < group) row = row_at(k0 + r);
         }
       }
-      j0 = j1;
-    } while (j0 < row.vecs);
-    for (int l = row.head + row.vecs * kE + tid; l < n; l += kThreads) scalar(l);
-    row = next;
-    if (a.keys) {
-      if (a.greedy && best_at >= 0) key = pack_key(best, (uint32_t)(c0 + best_at));
+    }
+    __syncthreads();
+
+    // The listed logits of these rows, after the copies of them. What the copy
+    // left in place of a masked one stays; in place, an allowed one's input is
+    // what the copy wrote.
+    const int listed = listed_count, items = listed * group;
+    for (int i0 = tid; i0 < items; i0 += threads * kListed) {
+      float x[kListed];
+      int id[kListed], of[kListed];
+      uint32_t word[kListed];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) key = max_key(key, __shfl_xor_sync(0xffffffffu, key, o));
-      // Two buffers: the row before last was read before the barrier of the last.
-      if (lane == 0) warp_best[k & 1][tid >> 5] = key;
-      __syncthreads();
-      if (tid == 0) {
-        for (int w = 1; w < kThreads / 32; ++w) key = max_key(key, warp_best[k & 1][w]);
-        a.keys[(b * rows + k) * p.stretches + stretch] = key;
+      for (int u = 0; u < kListed; ++u) {
+        const int item = min(i0 + u * threads, items - 1);
+        of[u] = item / listed;
+        id[u] = (int)list[item - of[u] * listed];
+        const int64_t k = k0 + of[u];
+        x[u] = to_f32((static_cast<const T*>(a.in) + b * a.in_batch + k * a.in_row + c0)[id[u]]);
+        word[u] = ~0u;
+        if (a.allowed) word[u] = (a.allowed + b * a.allowed_batch + k * a.allowed_row + (c0 >> 5))[id[u] >> 5];
       }
-    } else {
-      __syncthreads();  // the next draft token's count comes after this row's reads
+#pragma unroll
+      for (int u = 0; u < kListed; ++u) {
+        const int l = id[u];
+        if (i0 + u * threads >= items || !((word[u] >> (l & 31)) & 1u)) continue;
+        uint32_t times = (uint32_t)count[l];
+#pragma unroll
+        for (int d = 0; d < kRows - 1; ++d) times += d < of[u] && drafted[d] == l ? 1u : 0u;
+        float f = x[u];
+        if (times || bit(in_prompt, l)) f = f > 0.0f ? __fdiv_rn(f, rho) : __fmul_rn(f, rho);
+        if (times) f = __fsub_rn(__fsub_rn(f, __fmul_rn(freq, (float)times)), pres);
+        if (p.has_bias && slot[l]) f = __fadd_rn(f, bias[(uint32_t)slot[l] - 1u]);
+        const T y = from_f32<T>(f);
+        (static_cast<T*>(a.out) + b * a.out_batch + (k0 + of[u]) * a.out_row + c0)[l] = y;
+        if (a.keys) {
+          const unsigned long long mine =
+              a.greedy ? pack_key(to_f32(y), (uint32_t)(c0 + l)) : score(to_f32(y), k0 + of[u], l);
+          if (mine > *reinterpret_cast<volatile unsigned long long*>(&listed_key[of[u]])) atomicMax(&listed_key[of[u]], mine);
+        }
+      }
+    }
+    __syncthreads();
+    if (a.keys && tid < group) {
+      unsigned long long top = listed_key[tid];
+      for (int w = 0; w < threads / 32; ++w) top = max_key(top, warp_key[tid][w]);
+      a.keys[(b * rows + k0 + tid) * p.stretches + stretch] = top;
     }
   }
   if (bad) report_status(a.status, DSPARK_STATUS_TOKEN_RANGE);
@@ -380,62 +480,79 @@ __global__ void __launch_bounds__(32) choose_kernel(ConstrainArgs a, int stretch
   if (threadIdx.x == 0) a.tokens[row / a.block * a.tokens_batch + row % a.block] = (int64_t)key_token(best);
 }
 
-ConstrainPlan plan_constrain(const ConstrainArgs& a, int num_sms) {
-  ConstrainPlan p{};
-  p.has_bias = a.bias_count > 0 ? 1 : 0;
-  // Stretches small enough for two CTAs per SM's worth of them.
-  p.stretch = kMaxStretch;
-  p.shift = 13;
-  static_assert(kMaxStretch == 1 << 13, "the logarithm above");
-  while (p.stretch > kMinStretch && a.batch * ((a.vocab + p.stretch - 1) / p.stretch) < 2ll * num_sms) {
-    p.stretch /= 2;
-    --p.shift;
-  }
-  const int64_t stretches = (a.vocab + p.stretch - 1) / p.stretch;
-  p.cluster = 1;
-  while (p.cluster < 8 && a.history && a.history_cap > 512ll * p.cluster && stretches >= p.cluster * 2) p.cluster *= 2;
-  p.stretches = (int)((stretches + p.cluster - 1) / p.cluster * p.cluster);
-  return p;
+// The stretches for which the waves of CTAs take least. A CTA's cost, in ids:
+// its own ids for each row and once for the state, and a fixed part for its
+// start and the history, which all CTAs of a sequence read whole. CTAs that
+// share an SM share its rate.
+ConstrainPlan plan_constrain(const ConstrainArgs& a, int width, int num_sms) {
+  ConstrainPlan best{};
+  best.has_bias = a.bias_count > 0 ? 1 : 0;
+  int64_t best_cost = INT64_MAX;
+  const int64_t fixed = 4096 + (a.history ? a.history_cap / 4 : 0), passes = std::min<int64_t>(a.block, 1024) + 1;
+  const auto consider = [&](int64_t stretches) {
+    const int64_t least = (a.vocab + kMaxStretch - 1) / kMaxStretch;
+    stretches = std::max<int64_t>(least, std::min<int64_t>(stretches, (a.vocab + kMinStretch - 1) / kMinStretch));
+    const int64_t stretch = ((a.vocab + stretches - 1) / stretches + kMinStretch - 1) / kMinStretch * kMinStretch;
+    const int64_t real = (a.vocab + stretch - 1) / stretch;
+    const int64_t bytes = state_bytes(stretch, width, best.has_bias != 0);
+    if (bytes > kSmem) return;
+    const int64_t threads = std::min<int64_t>(kMaxThreads, std::max<int64_t>(64, stretch / 16)) / 32 * 32;
+    const int64_t per_sm = std::min<int64_t>(1024 / threads, (227 * 1024) / (bytes + 2304));
+    const int64_t waves = (a.batch * real + per_sm * num_sms - 1) / (per_sm * num_sms);
+    const int64_t shared = std::min(per_sm, (a.batch * real + num_sms - 1) / num_sms);
+    const int64_t cost = waves * shared * (fixed + stretch * passes);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best.stretch = (int)stretch;
+      best.stretches = (int)real;
+      best.threads = (int)threads;
+    }
+  };
+  for (int64_t ctas = 1; ctas <= 8; ++ctas) consider(ctas * num_sms / a.batch);  // per SM, in all
+  consider((a.vocab + kMaxStretch / 4 - 1) / (kMaxStretch / 4));
+  return best;
 }
 
-template <typename T>
-cudaError_t launch_typed(const ConstrainArgs& a, const ConstrainPlan& p, cudaStream_t s) {
-  const auto whole = [](const void* base, int64_t batch, int64_t row, const ConstrainArgs& c) {
+template <typename T, typename C>
+cudaError_t launch_typed(const ConstrainArgs& a, int num_sms, cudaStream_t s, ConstrainPlan* plan) {
+  const auto whole = [&a](const void* base, int64_t batch, int64_t row) {
     constexpr int64_t kE = Vec<T>::kE;
-    return reinterpret_cast<uintptr_t>(base) % 16 == 0 && (c.batch == 1 || batch % kE == 0) &&
-           (c.block == 1 || row % kE == 0);
+    return reinterpret_cast<uintptr_t>(base) % 16 == 0 && (a.batch == 1 || batch % kE == 0) &&
+           (a.block == 1 || row % kE == 0);
   };
-  const bool aligned = whole(a.in, a.in_batch, a.in_row, a) && whole(a.out, a.out_batch, a.out_row, a);
-  auto kernel = aligned ? constrain_kernel<T, true> : constrain_kernel<T, false>;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(a.batch * p.stretches));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)p.stretch / 8 + (size_t)p.stretch * 4 * (p.has_bias ? 2 : 1);
-  cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim = {(unsigned)p.cluster, 1, 1};
-  cfg.attrs = &attr;
-  cfg.numAttrs = p.cluster > 1 ? 1 : 0;
-  if (cfg.dynamicSmemBytes > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 68 * 1024);
+  const bool aligned = whole(a.in, a.in_batch, a.in_row) && whole(a.out, a.out_batch, a.out_row);
+  auto kernel = aligned ? constrain_kernel<T, C, true> : constrain_kernel<T, C, false>;
+  const ConstrainPlan p = plan_constrain(a, (int)sizeof(C), num_sms);
+  *plan = p;
+  if (a.batch * p.stretches > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  const size_t bytes = (size_t)state_bytes(p.stretch, (int)sizeof(C), p.has_bias != 0);
+  if (bytes > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
   }
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, p);
+  kernel<<<(unsigned)(a.batch * p.stretches), p.threads, bytes, s>>>(a, p);
   note_launch();
-  return e;
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 int64_t constrain_key_count(int64_t batch, int64_t block, int64_t vocab) {
-  return batch * block * ((vocab + kMinStretch - 1) / kMinStretch + 8);
+  return batch * block * ((vocab + kMinStretch - 1) / kMinStretch);
 }
 
 cudaError_t launch_constrain(const ConstrainArgs& a, int logits_dtype, int num_sms, cudaStream_t s) {
-  const ConstrainPlan p = plan_constrain(a, num_sms);
-  if (a.batch * p.stretches > 0x7fffffffll || a.batch * a.block > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  cudaError_t e = logits_dtype == DSPARK_DTYPE_FP32 ? launch_typed<float>(a, p, s) : launch_typed<__nv_bfloat16>(a, p, s);
+  if (a.batch * a.block > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  // The most that one id can count, and the largest bias entry.
+  const int64_t most = (a.history ? a.history_cap : 0) + a.draft_first + a.block;
+  const bool narrow = most <= 0xffff && a.bias_count <= 0xfffe;
+  ConstrainPlan p{};
+  cudaError_t e;
+  if (logits_dtype == DSPARK_DTYPE_FP32)
+    e = narrow ? launch_typed<float, uint16_t>(a, num_sms, s, &p) : launch_typed<float, uint32_t>(a, num_sms, s, &p);
+  else
+    e = narrow ? launch_typed<__nv_bfloat16, uint16_t>(a, num_sms, s, &p)
+               : launch_typed<__nv_bfloat16, uint32_t>(a, num_sms, s, &p);
   if (e != cudaSuccess || !a.keys) return e;
   choose_kernel<<<(unsigned)(a.batch * a.block), 32, 0, s>>>(a, p.stretches);
   note_launch();
