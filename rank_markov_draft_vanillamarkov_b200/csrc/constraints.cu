@@ -189,30 +189,19 @@ __global__ void __launch_bounds__(kMaxThreads, 2) constrain_kernel(ConstrainArgs
     return pack_key(y / a.temperature + noise_for(a.seed, (uint32_t)b, (uint32_t)(a.draft_first + k), v), v);
   };
 
-  // A row's place: elements before the first 16-byte address, vectors, and
-  // what is left.
-  struct Row {
-    const T* in;
-    T* out;
-    const uint32_t* mask;
-    int head, vecs;
-  };
-  auto row_at = [&](int64_t k) {
-    Row r;
-    r.in = static_cast<const T*>(a.in) + b * a.in_batch + k * a.in_row + c0;
-    r.out = static_cast<T*>(a.out) + b * a.out_batch + k * a.out_row + c0;
-    r.mask = a.allowed ? a.allowed + b * a.allowed_batch + k * a.allowed_row + (c0 >> 5) : nullptr;
-    r.head = 0;
-    if (!ALIGNED) {
-      const int past = (int)((reinterpret_cast<uintptr_t>(r.in) / sizeof(T)) % kE);
-      const bool same = (reinterpret_cast<uintptr_t>(r.in) - reinterpret_cast<uintptr_t>(r.out)) % 16 == 0;
-      r.head = same ? min(past ? kE - past : 0, n) : n;  // all single where the output's vectors lie elsewhere
-    }
-    r.vecs = (n - r.head) / kE;
-    return r;
+  // Rows are walked by pointers. A row's stretch is `head` elements before the
+  // first 16-byte address, `vecs` vectors, and what is left.
+    const T* const in0 = static_cast<const T*>(a.in) + b * a.in_batch + c0;
+  T* const out0 = static_cast<T*>(a.out) + b * a.out_batch + c0;
+  const uint32_t* const mask0 = a.allowed ? a.allowed + b * a.allowed_batch + (c0 >> 5) : nullptr;
+  auto head_of = [&](const T* in, const T* out) {
+    if (ALIGNED) return 0;
+    const int past = (int)((reinterpret_cast<uintptr_t>(in) / sizeof(T)) % kE);
+    const bool same = (reinterpret_cast<uintptr_t>(in) - reinterpret_cast<uintptr_t>(out)) % 16 == 0;
+    return same ? min(past ? kE - past : 0, n) : n;  // all single where the output's vectors lie elsewhere
   };
   // The thread's vectors of all rows in one stream: vector tid + q threads of
-  // row k, then the next q below `per_row`, then the next row. kInFlight of
+  // a row, then the next q below `per_row`, then the next row. kInFlight of
   // them are loaded ahead, the first while the state is built. A vector's mask
   // words are shifted when used: a use here would wait for the load.
   const int per_row = max(1, (n / kE + threads - 1) / threads);
@@ -221,92 +210,132 @@ __global__ void __launch_bounds__(kMaxThreads, 2) constrain_kernel(ConstrainArgs
     uint32_t lo, hi;
   };
   Loaded ahead[kInFlight];
-  int64_t load_k = 0;
-  int load_q = 0;
-  Row load_row = row_at(0);
+  const T* load_in = in0;
+  const T* load_out = out0;
+  const uint32_t* load_mask = mask0;
+  int64_t load_left = rows;
+  int load_q = per_row, load_j = tid, load_head = head_of(in0, out0);  // load_q counts down
   auto load = [&](Loaded& to) {
-    if (load_k >= rows) return;
-    const int j = tid + load_q * threads;
-    if (j < load_row.vecs) {
-      to.raw = __ldcs(reinterpret_cast<const uint4*>(load_row.in + load_row.head) + j);
-      if (load_row.mask) {
-        const int w = (load_row.head + j * kE) >> 5;
-        to.lo = load_row.mask[w];
-        if (!ALIGNED) to.hi = w < mask_last ? load_row.mask[w + 1] : 0u;
+    if (load_left <= 0) return;
+    if (load_j < (n - load_head) / kE) {
+      to.raw = __ldcs(reinterpret_cast<const uint4*>(load_in + load_head) + load_j);
+      if (load_mask) {
+        const int w = (load_head + load_j * kE) >> 5;
+        to.lo = load_mask[w];
+        if (!ALIGNED) to.hi = w < mask_last ? load_mask[w + 1] : 0u;
       }
     }
-    if (++load_q == per_row) {
-      load_q = 0;
-      if (++load_k < rows) load_row = row_at(load_k);
+    load_j += threads;
+    if (--load_q == 0) {
+      load_q = per_row;
+      load_j = tid;
+      --load_left;
+      load_in += a.in_row;
+      load_out += a.out_row;
+      load_head = head_of(load_in, load_out);
+      if (load_mask) load_mask += a.allowed_row;
     }
   };
 #pragma unroll
   for (int u = 0; u < kInFlight; ++u) load(ahead[u]);
 
-  // The state.
+  // The state. The first ids of the history and of the biases are read while
+  // the cells are cleared; the history's before its length is known, which its
+  // buffer covers.
   const int64_t cap = a.history ? a.history_cap : 0;
-  int64_t len = cap;
-  if (a.history && a.history_lens) len = min(max(a.history_lens[b], (int64_t)0), cap);
-  const int64_t prompt = a.prompt_lens ? min(max(a.prompt_lens[b], (int64_t)0), len) : 0;
+  const int64_t* history = a.history + b * a.history_stride;
+  const int64_t* bias_ids = a.bias_ids + b * a.bias_stride;
+  const int64_t* draft = a.draft ? a.draft + b * a.draft_stride : nullptr;
+  int64_t first_ids[kAhead / 2], first_bias = -1;
+#pragma unroll
+  for (int u = 0; u < kAhead / 2; ++u) first_ids[u] = tid + u * threads < cap ? history[tid + u * threads] : 0;
+  if (tid < a.bias_count) first_bias = bias_ids[tid];
+  int64_t len = a.history && a.history_lens ? a.history_lens[b] : cap;
+  int64_t prompt = a.prompt_lens ? a.prompt_lens[b] : 0;
   if (tid == 0) listed_count = 0;
   {
     uint4* cells = reinterpret_cast<uint4*>(in_prompt);
     const int vecs = (words * 4 + p.stretch * (int)sizeof(C) * (p.has_bias ? 2 : 1)) / 16;
     for (int i = tid; i < vecs; i += threads) cells[i] = make_uint4(0u, 0u, 0u, 0u);
   }
+  len = min(max(len, (int64_t)0), cap);
+  prompt = min(max(prompt, (int64_t)0), len);
   __syncthreads();
   bool bad = false;
-  auto scan = [&](const int64_t* ids, int64_t from, int64_t to, bool padded, auto note) {
-    for (int64_t i = from + tid; i < to; i += (int64_t)threads * kAhead) {
-      int64_t id[kAhead];
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) id[u] = i + u * threads < to ? ids[i + u * threads] : c0 + n;
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const uint64_t l = (uint64_t)(id[u] - c0);
-        if (l < (uint64_t)n) note((int)l, i + u * threads);
-        if (i + u * threads < to && (id[u] >= a.vocab || (id[u] < 0 && !padded))) bad = true;
-      }
+  auto note_token = [&](int64_t id, int64_t i) {
+    const uint64_t l = (uint64_t)(id - c0);
+    if (l < (uint64_t)n) {
+      if (i < prompt)
+        atomicOr(&in_prompt[l >> 5], 1u << (l & 31));
+      else
+        Cells<C>::add(count, (int)l);
     }
+    if ((uint64_t)id >= (uint64_t)a.vocab) bad = true;
   };
-  const int64_t* draft = a.draft ? a.draft + b * a.draft_stride : nullptr;
-  if (len > 0) {
-    const int64_t* history = a.history + b * a.history_stride;
-    scan(history, 0, prompt, false, [&](int l, int64_t) { atomicOr(&in_prompt[l >> 5], 1u << (l & 31)); });
-    scan(history, prompt, len, false, [&](int l, int64_t) { Cells<C>::add(count, l); });
-  }
-  if (draft) scan(draft, 0, a.draft_first, true, [&](int l, int64_t) { Cells<C>::add(count, l); });
-  if (p.has_bias)
-    scan(a.bias_ids + b * a.bias_stride, 0, a.bias_count, true,
-         [&](int l, int64_t i) { Cells<C>::keep_max(slot, l, (uint32_t)i + 1u); });
-  __syncthreads();
-  {
-    // A word of bits for each 32 ids, 32 words a warp at a time; lane i keeps
-    // word i, and the warp takes its places in the list at once.
-    for (int w0 = (tid >> 5) * 32; w0 < words; w0 += threads) {
-      const int here = min(32, words - w0);
-      uint32_t word = 0u;
-      for (int i = 0; i < here; ++i) {
-        const int l = (w0 + i) * 32 + lane;
-        const uint32_t bits = __ballot_sync(0xffffffffu, count[l] != 0 || (p.has_bias && slot[l] != 0));
-        if (lane == i) word = bits;
-      }
-      if (lane < here) {
-        word |= in_prompt[w0 + lane];
-        touched[w0 + lane] = word;
-      }
-      const int mine = __popc(word);
-      int sum = mine;
+  auto note_bias = [&](int64_t id, int64_t i) {
+    const uint64_t l = (uint64_t)(id - c0);
+    if (l < (uint64_t)n) Cells<C>::keep_max(slot, (int)l, (uint32_t)i + 1u);
+    if (id >= a.vocab) bad = true;
+  };
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int before = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += before;
-      }
-      int base = 0;
-      if (lane == 31 && sum) base = atomicAdd(&listed_count, sum);
-      base = __shfl_sync(0xffffffffu, base, 31) + sum - mine;
-      for (; word; word &= word - 1u) list[base++] = (uint16_t)((w0 + lane) * 32 + __ffs((int)word) - 1);
+  for (int u = 0; u < kAhead / 2; ++u)
+    if (tid + u * threads < len) note_token(first_ids[u], tid + u * threads);
+  for (int64_t i = tid + threads * (kAhead / 2); i < len; i += (int64_t)threads * kAhead) {
+    int64_t id[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) id[u] = i + u * threads < len ? history[i + u * threads] : 0;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (i + u * threads < len) note_token(id[u], i + u * threads);
+  }
+  if (draft) {
+    for (int64_t i = tid; i < a.draft_first; i += threads) {
+      const int64_t id = draft[i];
+      const uint64_t l = (uint64_t)(id - c0);
+      if (l < (uint64_t)n) Cells<C>::add(count, (int)l);
+      if (id >= a.vocab) bad = true;
     }
+  }
+  if (tid < a.bias_count) note_bias(first_bias, tid);
+  for (int64_t i = tid + threads; i < a.bias_count; i += threads) note_bias(bias_ids[i], i);
+  __syncthreads();
+  // A thread looks at 32 ids and keeps their bits; the warp then takes its
+  // places in the list at once.
+  for (int w0 = (tid >> 5) * 32; w0 < words; w0 += threads) {
+    const int w = w0 + lane;
+    uint32_t word = 0u;
+    if (w < words) {
+      word = in_prompt[w];
+      constexpr int kPer = 16 / sizeof(C);  // cells of 16 bytes
+      auto look = [&](const C* cells) {
+#pragma unroll
+        for (int i = 0; i < 32 / kPer; ++i) {
+          const uint4 x = *reinterpret_cast<const uint4*>(cells + w * 32 + i * kPer);
+          if (x.x | x.y | x.z | x.w) {
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+              const uint32_t v = sizeof(C) == 4 ? (e == 0 ? x.x : e == 1 ? x.y : e == 2 ? x.z : x.w)
+                                                : ((e < 2 ? x.x : e < 4 ? x.y : e < 6 ? x.z : x.w) >> (16 * (e & 1))) & 0xffffu;
+              if (v) word |= 1u << (i * kPer + e);
+            }
+          }
+        }
+      };
+      look(count);
+      if (p.has_bias) look(slot);
+      touched[w] = word;
+    }
+    const int mine = __popc(word);
+    int sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int before = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += before;
+    }
+    int base = 0;
+    if (lane == 31 && sum) base = atomicAdd(&listed_count, sum);
+    base = __shfl_sync(0xffffffffu, base, 31) + sum - mine;
+    for (; word; word &= word - 1u) list[base++] = (uint16_t)(w * 32 + __ffs((int)word) - 1);
   }
   const float rho = a.repetition ? a.repetition[b] : a.repetition_value;
   const float freq = a.frequency ? a.frequency[b] : a.frequency_value;
@@ -336,6 +365,10 @@ __global__ void __launch_bounds__(kMaxThreads, 2) constrain_kernel(ConstrainArgs
     if (tid < kRows) listed_key[tid] = 0ull;
     __syncthreads();
 
+    const T* in = in0 + k0 * a.in_row;
+    T* out = out0 + k0 * a.out_row;
+    const uint32_t* mask = mask0 ? mask0 + k0 * a.allowed_row : nullptr;
+
     // The copy. Greedy keys: the largest value so far, the vector (and its
     // first id) that holds it; a single element is a vector of its own. A row
     // of -inf alone keeps the first threads' own ids, of which the lowest
@@ -347,9 +380,9 @@ __global__ void __launch_bounds__(kMaxThreads, 2) constrain_kernel(ConstrainArgs
     unsigned long long key = 0ull;
     // Strictly larger, or the first NaN: ids rise, so equal values keep the lower one.
     auto better = [&](float y) { return y > best || (y != y && best == best); };
-    auto single = [&](const Row& row, int64_t k, int l) {
-      const T y = !row.mask || bit(row.mask, l) ? row.in[l] : from_f32<T>(-INFINITY);
-      row.out[l] = y;
+    auto single = [&](int64_t k, int l) {
+      const T y = !mask || bit(mask, l) ? in[l] : from_f32<T>(-INFINITY);
+      out[l] = y;
       if (!a.keys || bit(touched, l)) return;
       if (!a.greedy) {
         key = max_key(key, score(to_f32(y), k, l));
@@ -359,21 +392,20 @@ __global__ void __launch_bounds__(kMaxThreads, 2) constrain_kernel(ConstrainArgs
         best_single = true;
       }
     };
-    int r = 0, q = 0;
-    Row row = row_at(k0);
+    int r = 0, q = per_row, j = tid, head = head_of(in, out);  // q counts down
     while (r < group) {
 #pragma unroll
       for (int u = 0; u < kInFlight; ++u) {
         if (r >= group) break;
-        if (!ALIGNED && q == 0)
-          for (int l = tid; l < row.head; l += threads) single(row, k0 + r, l);
-        const int j = tid + q * threads, l = row.head + j * kE;
-        if (j < row.vecs) {
+        if (!ALIGNED && q == per_row)
+          for (int l = tid; l < head; l += threads) single(k0 + r, l);
+        const int l = head + j * kE;
+        if (j < (n - head) / kE) {
           uint4 raw = ahead[u].raw;
-          if (row.mask)
+          if (mask)
             raw = Vec<T>::masked(raw, ALIGNED ? ahead[u].lo >> (l & 31)
                                               : __funnelshift_r(ahead[u].lo, ahead[u].hi, l & 31));
-          __stcs(reinterpret_cast<uint4*>(row.out + row.head) + j, raw);
+          __stcs(reinterpret_cast<uint4*>(out + head) + j, raw);
           if (a.keys) {
             raw = Vec<T>::masked(raw, ~bits_at<ALIGNED>(touched, l, words - 1));
             if (a.greedy) {
@@ -391,8 +423,9 @@ __global__ void __launch_bounds__(kMaxThreads, 2) constrain_kernel(ConstrainArgs
           }
         }
         load(ahead[u]);
-        if (++q == per_row) {
-          for (int t = row.head + row.vecs * kE + tid; t < n; t += threads) single(row, k0 + r, t);
+        j += threads;
+        if (--q == 0) {
+          for (int t = head + (n - head) / kE * kE + tid; t < n; t += threads) single(k0 + r, t);
           if (a.keys) {
             if (a.greedy && best_at >= 0) {
               if (!best_single) {
@@ -415,8 +448,13 @@ __global__ void __launch_bounds__(kMaxThreads, 2) constrain_kernel(ConstrainArgs
             best_single = true;
             key = 0ull;
           }
-          q = 0;
-          if (++r < group) row = row_at(k0 + r);
+          q = per_row;
+          j = tid;
+          ++r;
+          in += a.in_row;
+          out += a.out_row;
+          if (mask) mask += a.allowed_row;
+          head = head_of(in, out);
         }
       }
     }
@@ -427,36 +465,38 @@ __global__ void __launch_bounds__(kMaxThreads, 2) constrain_kernel(ConstrainArgs
     // what the copy wrote.
     const int listed = listed_count, items = listed * group;
     for (int i0 = tid; i0 < items; i0 += threads * kListed) {
-      float x[kListed];
-      int id[kListed], of[kListed];
+      T x[kListed];
       uint32_t word[kListed];
 #pragma unroll
       for (int u = 0; u < kListed; ++u) {
-        const int item = min(i0 + u * threads, items - 1);
-        of[u] = item / listed;
-        id[u] = (int)list[item - of[u] * listed];
-        const int64_t k = k0 + of[u];
-        x[u] = to_f32((static_cast<const T*>(a.in) + b * a.in_batch + k * a.in_row + c0)[id[u]]);
-        word[u] = ~0u;
-        if (a.allowed) word[u] = (a.allowed + b * a.allowed_batch + k * a.allowed_row + (c0 >> 5))[id[u] >> 5];
+        const int item = min(i0 + u * threads, items - 1), g = item / listed;
+        const int64_t k = k0 + g;
+        const int l = (int)list[item - g * listed];
+        x[u] = in0[k * a.in_row + l];
+        word[u] = mask0 ? mask0[k * a.allowed_row + (l >> 5)] : ~0u;
       }
 #pragma unroll
       for (int u = 0; u < kListed; ++u) {
-        const int l = id[u];
-        if (i0 + u * threads >= items || !((word[u] >> (l & 31)) & 1u)) continue;
+        const int item = i0 + u * threads;
+        if (item >= items) break;
+        const int g = item / listed;
+        const int64_t k = k0 + g;
+        const int l = (int)list[item - g * listed];
+        if (!((word[u] >> (l & 31)) & 1u)) continue;
         uint32_t times = (uint32_t)count[l];
+        if (draft) {
 #pragma unroll
-        for (int d = 0; d < kRows - 1; ++d) times += d < of[u] && drafted[d] == l ? 1u : 0u;
-        float f = x[u];
+          for (int d = 0; d < kRows - 1; ++d) times += d < g && drafted[d] == l ? 1u : 0u;
+        }
+        float f = to_f32(x[u]);
         if (times || bit(in_prompt, l)) f = f > 0.0f ? __fdiv_rn(f, rho) : __fmul_rn(f, rho);
         if (times) f = __fsub_rn(__fsub_rn(f, __fmul_rn(freq, (float)times)), pres);
         if (p.has_bias && slot[l]) f = __fadd_rn(f, bias[(uint32_t)slot[l] - 1u]);
         const T y = from_f32<T>(f);
-        (static_cast<T*>(a.out) + b * a.out_batch + (k0 + of[u]) * a.out_row + c0)[l] = y;
+        out0[k * a.out_row + l] = y;
         if (a.keys) {
-          const unsigned long long mine =
-              a.greedy ? pack_key(to_f32(y), (uint32_t)(c0 + l)) : score(to_f32(y), k0 + of[u], l);
-          if (mine > *reinterpret_cast<volatile unsigned long long*>(&listed_key[of[u]])) atomicMax(&listed_key[of[u]], mine);
+          const unsigned long long mine = a.greedy ? pack_key(to_f32(y), (uint32_t)(c0 + l)) : score(to_f32(y), k, l);
+          if (mine > *reinterpret_cast<volatile unsigned long long*>(&listed_key[g])) atomicMax(&listed_key[g], mine);
         }
       }
     }
