@@ -288,10 +288,12 @@ typedef struct dspark_markov_constraints {
  *                   values like dspark_markov_sample_block's (temperature
  *                   below 1e-5: the lowest index of the largest; otherwise a
  *                   Gumbel-max draw at step draft_first + k of the seed).
- *   scratch         dspark_markov_constrain_scratch_bytes() bytes of device
- *                   memory, 8-byte aligned, needed where tokens is not NULL.
- *                   It may be reused once the call's work has run; calls that
- *                   overlap take one each.
+ *   scratch         dspark_markov_constrain_scratch_bytes(batch, block, vocab,
+ *                   history_cap (0 without a history), bias_count, draft_first
+ *                   + block - 1 (0 without drafted tokens), whether tokens is
+ *                   wanted) bytes of device memory, 16-byte aligned; NULL where
+ *                   that is 0. It may be reused once the call's work has run;
+ *                   calls that overlap take one each.
  *
  * An id at or above vocab (or a negative one inside a history) is left out and
  * sets DSPARK_STATUS_TOKEN_RANGE. batch == 0 or block == 0 is OK and enqueues
@@ -305,8 +307,9 @@ int dspark_markov_process_logits(const void* logits, void* out, int64_t batch, i
                                  int64_t* tokens, int64_t tokens_stride, float temperature, uint64_t seed,
                                  void* scratch, int32_t logits_dtype, void* stream);
 
-/* Scratch bytes of the calls that choose tokens under constraints; 0 for sizes they refuse. */
-int64_t dspark_markov_constrain_scratch_bytes(int64_t batch, int64_t block, int64_t vocab);
+/* Scratch bytes of the calls under constraints; 0 for sizes they refuse. */
+int64_t dspark_markov_constrain_scratch_bytes(int64_t batch, int64_t block, int64_t vocab, int64_t history_cap,
+                                              int64_t bias_count, int64_t draft_tokens, int32_t choose);
 
 /*
  * dspark_markov_sample_block under token constraints: position k's corrected
@@ -316,8 +319,8 @@ int64_t dspark_markov_constrain_scratch_bytes(int64_t batch, int64_t block, int6
  * (the tensor-core or the generic kernels as for
  * dspark_markov_apply_block_logits), so constraints cost launches that the
  * unconstrained sampler does not have. `allowed` rows are those of the block's
- * positions; scratch as for (batch, 1, vocab), so that calls that overlap take
- * one each. Other arguments, ownership and errors as for
+ * positions; scratch as for (batch, 1, vocab, history_cap, bias_count,
+ * proposal_len, 1), and calls that overlap take one each. Other arguments, ownership and errors as for
  * dspark_markov_sample_block.
  */
 int dspark_markov_sample_block_constrained(const void* base_logits, const int64_t* first_prev_token_ids,

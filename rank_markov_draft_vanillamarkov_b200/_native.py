@@ -73,7 +73,7 @@ SIGNATURES = {
                                                           _vp, _vp, _i32, _i32, _vp]),
     "dspark_markov_process_logits": (ctypes.c_int, [_vp, _vp, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _i64,
                                                     _i64, _vp, _i64, _i64, _vp, _i64, _f32, _u64, _vp, _i32, _vp]),
-    "dspark_markov_constrain_scratch_bytes": (_i64, [_i64, _i64, _i64]),
+    "dspark_markov_constrain_scratch_bytes": (_i64, [_i64, _i64, _i64, _i64, _i64, _i64, _i32]),
     "dspark_markov_sample_block_constrained": (ctypes.c_int, [_vp, _vp, _i64, _i64, _i64, _vp, _vp, _i32, _f32, _u64,
                                                               _vp, _vp, _i64, _i64, _vp, _vp, _vp, _i32, _i32, _vp]),
     "dspark_markov_block_cross_entropy": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _vp,

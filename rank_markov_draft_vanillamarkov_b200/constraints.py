@@ -103,6 +103,18 @@ class TokenConstraints:
             c.bias_ids, c.bias_values = bias_ids.data_ptr(), bias_values.data_ptr()
         self._c = c
         self._ref = ctypes.byref(c)
+        self._sizes = {}
+
+    def _scratch(self, device: torch.device, batch: int, block: int, drafted: int, choose: bool) -> Optional[torch.Tensor]:
+        """Working memory of one call, its size kept by the call's sizes."""
+        key = (batch, block, drafted, choose)
+        size = self._sizes.get(key)
+        if size is None:
+            size = N.load().dspark_markov_constrain_scratch_bytes(
+                batch, block, self.vocab_size, self._c.history_cap, self._c.bias_count, drafted, choose)
+            if len(self._sizes) < 256:
+                self._sizes[key] = size
+        return torch.empty(size, dtype=torch.uint8, device=device) if size else None
 
     def _take(self, t: torch.Tensor, name: str, rows: Optional[int], strided: bool = False) -> None:
         if not t.is_cuda or (self.device is not None and t.device != self.device):
@@ -193,7 +205,7 @@ def process_logits(logits: torch.Tensor, constraints: TokenConstraints, *,
         _check_cuda(draft_tokens, "draft_tokens", device)
         draft = draft_tokens.data_ptr()
     mask, mask_batch, mask_row = _allowed_args(allowed, batch, block, vocab, device)
-    tokens = scratch = None
+    tokens = None
     if return_tokens or out_tokens is not None:
         if out_tokens is None:
             tokens = torch.empty(logits.shape[:-1], dtype=torch.int64, device=device)
@@ -206,9 +218,7 @@ def process_logits(logits: torch.Tensor, constraints: TokenConstraints, *,
         return out, tokens
     lib = N.load()
     with _device_guard(device):
-        if tokens is not None:
-            scratch = torch.empty(lib.dspark_markov_constrain_scratch_bytes(batch, block, vocab), dtype=torch.uint8,
-                                  device=device)
+        scratch = constraints._scratch(device, batch, block, block - 1 if draft is not None else 0, tokens is not None)
         code = lib.dspark_markov_process_logits(
             logits.data_ptr(), out.data_ptr(), batch, block, vocab, istride[0], istride[1] if dim == 3 else vocab,
             ostride[0], ostride[1] if dim == 3 else vocab, constraints._ref, draft, block, 0, mask, mask_batch,

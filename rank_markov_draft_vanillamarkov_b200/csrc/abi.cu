@@ -193,6 +193,14 @@ bool constraints_ok(const dspark_markov_constraints* c) {
   return true;
 }
 
+// Sizes that ids, counts and offsets of the kernels hold.
+bool constrain_sizes_ok(int64_t batch, int64_t block, int64_t vocab, int64_t history_cap, int64_t bias_count,
+                        int64_t draft_tokens) {
+  constexpr int64_t kMost = 0x7fffffffll;
+  return vocab <= 0x7ffffe00ll && bounded(batch, block, 0, kMost) >= 0 && bounded(batch, vocab / 512 + 1, 0, kMost) >= 0 &&
+         history_cap <= 0x3fffffffll && bias_count <= 0x3fffffffll && draft_tokens <= 0x3fffffffll;
+}
+
 ConstrainArgs constrain_args(const dspark_markov_constraints& c) {
   ConstrainArgs a{};
   a.history = c.history_cap > 0 ? c.history : nullptr;
@@ -539,10 +547,22 @@ int dspark_markov_sample_block_noalloc(const void* base_logits, const int64_t* f
   return cuda_code(e);
 }
 
-int64_t dspark_markov_constrain_scratch_bytes(int64_t batch, int64_t block, int64_t vocab) {
-  if (batch <= 0 || block <= 0 || vocab <= 0 || vocab > 0xfffffffell) return 0;
-  if (bounded(batch, block, 0, 0x7fffffffll) < 0) return 0;
-  return constrain_key_count(batch, block, vocab) * (int64_t)sizeof(unsigned long long);
+int64_t dspark_markov_constrain_scratch_bytes(int64_t batch, int64_t block, int64_t vocab, int64_t history_cap,
+                                              int64_t bias_count, int64_t draft_tokens, int32_t choose) {
+  if (batch <= 0 || block <= 0 || vocab <= 0 || history_cap < 0 || bias_count < 0 || draft_tokens < 0 ||
+      !constrain_sizes_ok(batch, block, vocab, history_cap, bias_count, draft_tokens))
+    return 0;
+  ConstrainArgs a{};
+  int64_t unused = 0;  // pointers only say what is there
+  a.batch = batch;
+  a.block = block;
+  a.vocab = vocab;
+  a.history = history_cap ? &unused : nullptr;
+  a.history_cap = history_cap;
+  a.bias_count = bias_count;
+  a.draft_most = draft_tokens;
+  a.tokens = choose ? &unused : nullptr;
+  return constrain_scratch_bytes(a);
 }
 
 int dspark_markov_process_logits(const void* logits, void* out, int64_t batch, int64_t block, int64_t vocab,
@@ -559,14 +579,16 @@ int dspark_markov_process_logits(const void* logits, void* out, int64_t batch, i
       allowed_row_stride < 0 || tokens_stride < 0)
     return DSPARK_ERR_INVALID_ARG;
   if (batch == 0 || block == 0) return DSPARK_OK;
-  if (!logits || !out || (tokens && !scratch)) return DSPARK_ERR_INVALID_ARG;
-  if (vocab > 0xfffffffell || bounded(batch, block, 0, 0x7fffffffll) < 0 || draft_first > 0x7fffffffll - block)
+  if (!logits || !out) return DSPARK_ERR_INVALID_ARG;
+  if (draft_first > 0x3fffffffll) return DSPARK_ERR_UNSUPPORTED;
+  const int64_t drafts = draft_tokens ? draft_first + block - 1 : 0;
+  if (!constrain_sizes_ok(batch, block, vocab, constraints->history_cap, constraints->bias_count, drafts))
     return DSPARK_ERR_UNSUPPORTED;
   const size_t lsize = logits_dtype == DSPARK_DTYPE_BF16 ? 2 : 4;
   const int64_t n_in = extent(batch, block, vocab, in_batch_stride, in_row_stride);
   const int64_t n_out = extent(batch, block, vocab, out_batch_stride, out_row_stride);
   if (n_in < 0 || n_out < 0 || !disjoint_rows(batch, block, vocab, out_batch_stride, out_row_stride) ||
-      !aligned_to(logits, lsize) || !aligned_to(out, lsize) || !aligned_to(scratch, 8))
+      !aligned_to(logits, lsize) || !aligned_to(out, lsize) || !aligned_to(scratch, 16))
     return DSPARK_ERR_INVALID_ARG;
   if (tokens && batch > 1 && tokens_stride < block) return DSPARK_ERR_INVALID_ARG;
   if (draft_tokens && batch > 1 && draft_stride < draft_first + block - 1) return DSPARK_ERR_INVALID_ARG;
@@ -596,15 +618,17 @@ int dspark_markov_process_logits(const void* logits, void* out, int64_t batch, i
   a.allowed = static_cast<const uint32_t*>(allowed);
   a.allowed_batch = allowed_batch_stride;
   a.allowed_row = allowed_row_stride;
-  a.keys = tokens ? static_cast<unsigned long long*>(scratch) : nullptr;
+  a.draft_most = drafts;
+  a.scratch = scratch;
   a.tokens = tokens;
   a.tokens_batch = tokens_stride;
   a.greedy = !(temperature >= 1e-5f) ? 1 : 0;
   a.temperature = temperature;
   a.seed = seed;
   a.status = d->status;
+  if (!scratch && constrain_scratch_bytes(a) > 0) return DSPARK_ERR_INVALID_ARG;
   t_last_algo = 1;
-  return cuda_code(launch_constrain(a, logits_dtype, d->num_sms, static_cast<cudaStream_t>(stream)));
+  return cuda_code(launch_constrain(a, logits_dtype, static_cast<cudaStream_t>(stream)));
 }
 
 int dspark_markov_sample_block_constrained(const void* base_logits, const int64_t* first_prev_token_ids,
@@ -622,9 +646,10 @@ int dspark_markov_sample_block_constrained(const void* base_logits, const int64_
     return DSPARK_ERR_INVALID_ARG;
   if (batch == 0 || proposal_len == 0) return DSPARK_OK;
   if (!base_logits || !first_prev_token_ids || !w1 || !w2 || !sampled_tokens || !corrected_logits || !scratch ||
-      !aligned_to(scratch, 8))
+      !aligned_to(scratch, 16))
     return DSPARK_ERR_INVALID_ARG;
-  if (vocab > 0xfffffffell || bounded(batch, proposal_len, 0, 0x7fffffffll) < 0) return DSPARK_ERR_UNSUPPORTED;
+  if (!constrain_sizes_ok(batch, proposal_len, vocab, constraints->history_cap, constraints->bias_count, proposal_len))
+    return DSPARK_ERR_UNSUPPORTED;
   const size_t lsize = logits_dtype == DSPARK_DTYPE_BF16 ? 2 : 4;
   const int64_t n = extent(batch, proposal_len, vocab, proposal_len * vocab, vocab);
   const uintptr_t a0 = reinterpret_cast<uintptr_t>(base_logits), c0 = reinterpret_cast<uintptr_t>(corrected_logits);
@@ -650,7 +675,8 @@ int dspark_markov_sample_block_constrained(const void* base_logits, const int64_
   c.draft = sampled_tokens;
   c.draft_stride = proposal_len;
   c.allowed_batch = allowed_batch_stride;
-  c.keys = static_cast<unsigned long long*>(scratch);
+  c.draft_most = proposal_len;
+  c.scratch = scratch;
   c.tokens_batch = proposal_len;
   c.greedy = !(temperature >= 1e-5f) ? 1 : 0;
   c.temperature = temperature;
@@ -676,7 +702,7 @@ int dspark_markov_sample_block_constrained(const void* base_logits, const int64_
     c.draft_first = k;
     c.allowed = allowed ? static_cast<const uint32_t*>(allowed) + k * allowed_row_stride : nullptr;
     c.tokens = sampled_tokens + k;
-    e = launch_constrain(c, logits_dtype, d->num_sms, s);
+    e = launch_constrain(c, logits_dtype, s);
     if (e != cudaSuccess) return DSPARK_ERR_CUDA;
   }
   return DSPARK_OK;

@@ -11,17 +11,22 @@
 // each operation in fp32, one rounding to the logits dtype at the end.
 //
 // Almost every logit only passes through, so the bound is the copy: 4 bytes
-// per bf16 logit and an eighth of a byte of mask. A CTA takes one stretch of
-// the vocabulary of one sequence and walks that sequence's rows over it. It
-// first builds the stretch's state in shared memory from the whole history
-// (which comes from L2 for all but the first): a count and a prompt bit per
-// id, the last bias entry of each id, and a list of the ids that have any of
-// these or are drafted. Rows then go by 16-byte vectors, masked and copied,
-// eight rows at a time, and the few listed logits of all eight are worked out
-// afterwards, one thread for each; within the copy they would cost every warp
-// the whole arithmetic for a lane or two.
+// per bf16 logit and an eighth of a byte of mask. Two kernels:
+//
+//   list_kernel  finds the ids of each sequence that have a state at all (in
+//                the history, biased, drafted) and writes them with it, in
+//                order of the ids. A CTA takes a part of the vocabulary, as
+//                much as its shared memory can count, and reads the history.
+//   copy_kernel  masks and copies the rows by 16-byte vectors, a stretch of
+//                the vocabulary of one sequence per CTA and up to eight rows
+//                at a time, then works out the listed logits of those rows,
+//                one thread for each. Within the copy they would cost every
+//                warp the whole arithmetic for a lane or two, and counting in
+//                each of the many CTAs that a copy needs cost more than the
+//                copy (67 us for 32 x 8 rows of 151936 bf16).
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -31,27 +36,32 @@ namespace dspark {
 
 namespace {
 
-constexpr int kMaxThreads = 512;
-constexpr int kInFlight = 4;       // vectors under way per thread
-constexpr int kRows = 8;           // rows copied before their listed logits are worked out
-constexpr int kListed = 4;         // listed logits in flight per thread
+constexpr int kBlock = 512;        // ids; the unit of parts and stretches, with a place of its own in the lists
+constexpr int kListThreads = 1024;
+constexpr int kRounds = 4;         // words of 32 ids per thread of list_kernel, at most
+constexpr int kMaxPart = kListThreads * kRounds * 32;
+constexpr int kListSmem = 222 * 1024;
 constexpr int kAhead = 8;          // history ids in flight per thread
-constexpr int kMinStretch = 512;   // ids
-constexpr int kMaxStretch = 32256;
-constexpr int kSmem = 222 * 1024;  // dynamic shared memory of a CTA, at most
+constexpr int kCopyThreads = 512;
+constexpr int kMaxStretch = 32768;
+constexpr int kInFlight = 4;       // vectors, or listed logits, under way per thread
+constexpr int kRows = 8;           // rows copied before their listed logits are worked out
+template <int N>
+using Int = std::integral_constant<int, N>;
 
+constexpr uint32_t kFlag = 0x80000000u;  // of an entry's id: biased; of its count: in the prompt
+
+// The sizes of both kernels and the places in the scratch, for one call.
 struct ConstrainPlan {
-  int stretch;    // ids per CTA, a multiple of kMinStretch
-  int stretches;  // per sequence
-  int threads;    // per CTA
-  int has_bias;
+  int has_bias, narrow;
+  int part, parts, list_threads;  // ids per CTA of list_kernel, per sequence; parts 0: nothing is listed
+  int stretch, stretches, copy_threads;
+  int64_t entries;                // places for entries per part
+  // Byte offsets in the scratch: [rows] keys and [batch] counters, both cleared
+  // by list_kernel; per part, the number of entries before each block and in
+  // all; entries as planes of ids, counts and biases.
+  int64_t counters, before, ids, counts, biases, bytes;
 };
-
-// Bytes of state per kMinStretch ids: counts and bias entries of W bytes each,
-// the list, prompt and touched bits.
-constexpr int64_t state_bytes(int64_t stretch, int width, bool has_bias) {
-  return stretch * (width * (has_bias ? 2 : 1) + 2) + stretch / 8 * 2;
-}
 
 // An array of counts, or of the last entry of each id, in shared memory.
 // 16-bit elements share the atomics of their 32-bit word.
@@ -89,6 +99,182 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t* words, int at, int l
   return __funnelshift_r(lo, hi, at & 31);
 }
 __device__ __forceinline__ bool bit(const uint32_t* words, int at) { return (words[at >> 5] >> (at & 31)) & 1u; }
+
+template <typename P>
+__device__ __forceinline__ P* plane(const ConstrainArgs& a, int64_t offset) {
+  return reinterpret_cast<P*>(static_cast<unsigned char*>(a.scratch) + offset);
+}
+
+// C: uint16_t where no count nor bias entry passes 65535, else uint32_t.
+template <typename C>
+__global__ void __launch_bounds__(kListThreads, 1) list_kernel(ConstrainArgs a, ConstrainPlan p) {
+  extern __shared__ __align__(16) uint32_t smem[];
+  __shared__ int totals[kRounds * kListThreads / 32 + 1];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = (int)blockDim.x, warps = threads >> 5;
+  const int64_t b = blockIdx.x / p.parts;
+  const int part = (int)(blockIdx.x % p.parts);
+  const int64_t c0 = (int64_t)part * p.part;
+  const int n = (int)min((int64_t)p.part, a.vocab - c0), words = p.part / 32;
+  uint32_t* in_prompt = smem;            // one bit per id
+  uint32_t* in_block = smem + words;     // drafted in this block
+  C* count = reinterpret_cast<C*>(smem + 2 * words);
+  C* slot = count + p.part;              // last bias entry + 1, where there are biases
+  // The first ids of the history are read while the cells are cleared, before
+  // its length is known: its buffer covers them.
+  const int cap = a.history ? (int)a.history_cap : 0;
+  const int64_t* history = a.history + b * a.history_stride;
+  const int64_t* bias_ids = a.bias_ids + b * a.bias_stride;
+  const int64_t* draft = a.draft ? a.draft + b * a.draft_stride : nullptr;
+  int64_t first_ids[kAhead], first_bias = -1;
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) first_ids[u] = tid + u * threads < cap ? history[tid + u * threads] : 0;
+  if (tid < a.bias_count) first_bias = bias_ids[tid];
+  int64_t length = a.history && a.history_lens ? a.history_lens[b] : cap;
+  int64_t prompted = a.prompt_lens ? a.prompt_lens[b] : 0;
+  {
+    uint4* cells = reinterpret_cast<uint4*>(smem);
+    const int vecs = (words * 8 + p.part * (int)sizeof(C) * (p.has_bias ? 2 : 1)) / 16;
+    for (int i = tid; i < vecs; i += threads) cells[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  if (part == 0 && a.tokens) {
+    if (tid == 0) plane<uint32_t>(a, p.counters)[b] = 0u;
+    for (int64_t k = tid; k < a.block; k += threads) plane<unsigned long long>(a, 0)[b * a.block + k] = 0ull;
+  }
+  const int len = (int)min(max(length, (int64_t)0), (int64_t)cap);
+  const int prompt = (int)min(max(prompted, (int64_t)0), (int64_t)len);
+  __syncthreads();
+  bool bad = false;
+  auto note_token = [&](int64_t id, int i) {
+    const uint64_t l = (uint64_t)(id - c0);
+    if (l < (uint64_t)n) {
+      if (i < prompt)
+        atomicOr(&in_prompt[l >> 5], 1u << (l & 31));
+      else
+        Cells<C>::add(count, (int)l);
+    }
+    if ((uint64_t)id >= (uint64_t)a.vocab) bad = true;
+  };
+  auto note_bias = [&](int64_t id, int64_t i) {
+    const uint64_t l = (uint64_t)(id - c0);
+    if (l < (uint64_t)n) Cells<C>::keep_max(slot, (int)l, (uint32_t)i + 1u);
+    if (id >= a.vocab) bad = true;
+  };
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (tid + u * threads < len) note_token(first_ids[u], tid + u * threads);
+  for (int i = tid + threads * kAhead; i < len; i += threads * kAhead) {
+    int64_t id[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) id[u] = i + u * threads < len ? history[i + u * threads] : 0;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (i + u * threads < len) note_token(id[u], i + u * threads);
+  }
+  if (tid < a.bias_count) note_bias(first_bias, tid);
+  for (int64_t i = tid + threads; i < a.bias_count; i += threads) note_bias(bias_ids[i], i);
+  if (draft) {
+    // Those before the block count; those of the block are listed, and counted
+    // row by row later. The last row's own token precedes no row.
+    for (int64_t i = tid; i < a.draft_first + a.block - 1; i += threads) {
+      const int64_t id = draft[i];
+      const uint64_t l = (uint64_t)(id - c0);
+      if (id >= a.vocab) bad = true;
+      if (l >= (uint64_t)n) continue;
+      if (i < a.draft_first)
+        Cells<C>::add(count, (int)l);
+      else
+        atomicOr(&in_block[l >> 5], 1u << (l & 31));
+    }
+  }
+  __syncthreads();
+
+  // A word of 32 ids per lane and round, in order of the ids over rounds, warps
+  // and lanes.
+  uint32_t word[kRounds];
+  int mine[kRounds];  // entries before the lane's within the warp's words
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const int w = (r * warps + warp) * 32 + lane;
+    word[r] = 0u;
+    if (w < words) {
+      word[r] = in_prompt[w] | in_block[w];
+      constexpr int kPer = 16 / sizeof(C);  // cells of 16 bytes
+      auto look = [&](const C* cells) {
+#pragma unroll
+        for (int i = 0; i < 32 / kPer; ++i) {
+          const uint4 x = *reinterpret_cast<const uint4*>(cells + w * 32 + i * kPer);
+          if (x.x | x.y | x.z | x.w) {
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+              const uint32_t v = sizeof(C) == 4 ? (e == 0 ? x.x : e == 1 ? x.y : e == 2 ? x.z : x.w)
+                                                : ((e < 2 ? x.x : e < 4 ? x.y : e < 6 ? x.z : x.w) >> (16 * (e & 1))) & 0xffffu;
+              if (v) word[r] |= 1u << (i * kPer + e);
+            }
+          }
+        }
+      };
+      look(count);
+      if (p.has_bias) look(slot);
+    }
+    int sum = __popc(word[r]);
+    mine[r] = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int before = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += before;
+    }
+    mine[r] = sum - mine[r];
+    if (lane == 31) totals[r * warps + warp] = sum;
+  }
+  __syncthreads();
+  if (warp == 0) {  // totals of warps before each, and of all
+    int carry = 0;
+    for (int i0 = 0; i0 < kRounds * warps; i0 += 32) {
+      const int own = i0 + lane < kRounds * warps ? totals[i0 + lane] : 0;
+      int sum = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int before = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += before;
+      }
+      if (i0 + lane < kRounds * warps) totals[i0 + lane] = carry + sum - own;
+      carry += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) totals[kRounds * warps] = carry;
+  }
+  __syncthreads();
+
+  const int blocks = p.part / kBlock;
+  const int64_t which = b * p.parts + part;
+  uint32_t* before = plane<uint32_t>(a, p.before) + which * (blocks + 1);
+  uint32_t* ids = plane<uint32_t>(a, p.ids) + which * p.entries;
+  uint32_t* counts = plane<uint32_t>(a, p.counts) + which * p.entries;
+  float* biases = plane<float>(a, p.biases) + which * p.entries;
+  const float* bias = a.bias_values + b * a.bias_stride;
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const int w0 = (r * warps + warp) * 32, base = totals[r * warps + warp];
+    if (w0 + lane < words && (w0 + lane) % (kBlock / 32) == 0)
+      before[(w0 + lane) / (kBlock / 32)] = (uint32_t)(base + mine[r]);
+    // The warp's words one after another, a lane per id.
+    uint32_t some = __ballot_sync(0xffffffffu, word[r] != 0u);
+    for (; some; some &= some - 1u) {
+      const int from = __ffs((int)some) - 1;
+      const uint32_t bits = __shfl_sync(0xffffffffu, word[r], from);
+      const int at = base + __shfl_sync(0xffffffffu, mine[r], from) + __popc(bits & ((1u << lane) - 1u));
+      if ((bits >> lane) & 1u) {
+        const int l = (w0 + from) * 32 + lane;
+        const uint32_t entry = p.has_bias ? (uint32_t)slot[l] : 0u;
+        ids[at] = (uint32_t)(c0 + l) | (entry ? kFlag : 0u);
+        counts[at] = (uint32_t)count[l] | (bit(in_prompt, l) ? kFlag : 0u);
+        if (entry) biases[at] = bias[entry - 1u];
+      }
+    }
+  }
+  if (tid == 0) before[blocks] = (uint32_t)totals[kRounds * warps];
+  if (bad) report_status(a.status, DSPARK_STATUS_TOKEN_RANGE);
+}
 
 // Bits 0..3 of n as all-ones or zero halves of two words: element 2i in the
 // low half of word i. The product spreads the bits to the signs of four bytes
@@ -164,34 +350,29 @@ __device__ __forceinline__ unsigned long long max_key(unsigned long long a, unsi
   return a > b ? a : b;
 }
 
-// C: uint16_t where no count nor bias entry passes 65535, else uint32_t.
 // ALIGNED: every row starts at a 16-byte address, in and out.
-template <typename T, typename C, bool ALIGNED>
-__global__ void __launch_bounds__(kMaxThreads, 2) constrain_kernel(ConstrainArgs a, ConstrainPlan p) {
+template <typename T, bool ALIGNED>
+__global__ void __launch_bounds__(kCopyThreads, 2) copy_kernel(ConstrainArgs a, ConstrainPlan p) {
   constexpr int kE = Vec<T>::kE;
-  extern __shared__ __align__(16) uint32_t smem[];
-  __shared__ int drafted[kRows];  // local ids (-1: elsewhere) of the tokens drafted after each of the rows
-  __shared__ unsigned long long warp_key[kRows][kMaxThreads / 32], listed_key[kRows];
-  __shared__ int listed_count;
+  extern __shared__ __align__(16) uint32_t touched[];  // one bit per id of the stretch: listed
+  __shared__ int drafted[kRows];  // the tokens drafted after each of the rows (-1: none)
+  __shared__ unsigned long long warp_key[kRows][kCopyThreads / 32], listed_key[kRows];
+  __shared__ bool last;
   const int tid = (int)threadIdx.x, lane = tid & 31, threads = (int)blockDim.x;
   const int64_t b = blockIdx.x / p.stretches;
   const int stretch = (int)(blockIdx.x % p.stretches);
   const int64_t c0 = (int64_t)stretch * p.stretch, rows = a.block;
   const int n = (int)min((int64_t)p.stretch, a.vocab - c0);
   const int words = p.stretch / 32, mask_last = (n + 31) / 32 - 1;
-  uint32_t* touched = smem;
-  uint32_t* in_prompt = touched + words;
-  C* count = reinterpret_cast<C*>(in_prompt + words);
-  C* slot = count + p.stretch;  // where there are biases
-  uint16_t* list = reinterpret_cast<uint16_t*>(slot + (p.has_bias ? p.stretch : 0));
+  const bool keyed = a.tokens != nullptr;
   auto score = [&](float y, int64_t k, int l) {
     const uint32_t v = (uint32_t)(c0 + l);
     return pack_key(y / a.temperature + noise_for(a.seed, (uint32_t)b, (uint32_t)(a.draft_first + k), v), v);
   };
 
   // Rows are walked by pointers. A row's stretch is `head` elements before the
-  // first 16-byte address, `vecs` vectors, and what is left.
-    const T* const in0 = static_cast<const T*>(a.in) + b * a.in_batch + c0;
+  // first 16-byte address, whole vectors, and what is left.
+  const T* const in0 = static_cast<const T*>(a.in) + b * a.in_batch + c0;
   T* const out0 = static_cast<T*>(a.out) + b * a.out_batch + c0;
   const uint32_t* const mask0 = a.allowed ? a.allowed + b * a.allowed_batch + (c0 >> 5) : nullptr;
   auto head_of = [&](const T* in, const T* out) {
@@ -202,8 +383,8 @@ __global__ void __launch_bounds__(kMaxThreads, 2) constrain_kernel(ConstrainArgs
   };
   // The thread's vectors of all rows in one stream: vector tid + q threads of
   // a row, then the next q below `per_row`, then the next row. kInFlight of
-  // them are loaded ahead, the first while the state is built. A vector's mask
-  // words are shifted when used: a use here would wait for the load.
+  // them are loaded ahead. A vector's mask words are shifted when used: a use
+  // here would wait for the load.
   const int per_row = max(1, (n / kE + threads - 1) / threads);
   struct Loaded {
     uint4 raw;
@@ -239,132 +420,44 @@ __global__ void __launch_bounds__(kMaxThreads, 2) constrain_kernel(ConstrainArgs
 #pragma unroll
   for (int u = 0; u < kInFlight; ++u) load(ahead[u]);
 
-  // The state. The first ids of the history and of the biases are read while
-  // the cells are cleared; the history's before its length is known, which its
-  // buffer covers.
-  const int64_t cap = a.history ? a.history_cap : 0;
-  const int64_t* history = a.history + b * a.history_stride;
-  const int64_t* bias_ids = a.bias_ids + b * a.bias_stride;
-  const int64_t* draft = a.draft ? a.draft + b * a.draft_stride : nullptr;
-  int64_t first_ids[kAhead / 2], first_bias = -1;
-#pragma unroll
-  for (int u = 0; u < kAhead / 2; ++u) first_ids[u] = tid + u * threads < cap ? history[tid + u * threads] : 0;
-  if (tid < a.bias_count) first_bias = bias_ids[tid];
-  int64_t len = a.history && a.history_lens ? a.history_lens[b] : cap;
-  int64_t prompt = a.prompt_lens ? a.prompt_lens[b] : 0;
-  if (tid == 0) listed_count = 0;
-  {
-    uint4* cells = reinterpret_cast<uint4*>(in_prompt);
-    const int vecs = (words * 4 + p.stretch * (int)sizeof(C) * (p.has_bias ? 2 : 1)) / 16;
-    for (int i = tid; i < vecs; i += threads) cells[i] = make_uint4(0u, 0u, 0u, 0u);
-  }
-  len = min(max(len, (int64_t)0), cap);
-  prompt = min(max(prompt, (int64_t)0), len);
-  __syncthreads();
-  bool bad = false;
-  auto note_token = [&](int64_t id, int64_t i) {
-    const uint64_t l = (uint64_t)(id - c0);
-    if (l < (uint64_t)n) {
-      if (i < prompt)
-        atomicOr(&in_prompt[l >> 5], 1u << (l & 31));
-      else
-        Cells<C>::add(count, (int)l);
-    }
-    if ((uint64_t)id >= (uint64_t)a.vocab) bad = true;
-  };
-  auto note_bias = [&](int64_t id, int64_t i) {
-    const uint64_t l = (uint64_t)(id - c0);
-    if (l < (uint64_t)n) Cells<C>::keep_max(slot, (int)l, (uint32_t)i + 1u);
-    if (id >= a.vocab) bad = true;
-  };
-#pragma unroll
-  for (int u = 0; u < kAhead / 2; ++u)
-    if (tid + u * threads < len) note_token(first_ids[u], tid + u * threads);
-  for (int64_t i = tid + threads * (kAhead / 2); i < len; i += (int64_t)threads * kAhead) {
-    int64_t id[kAhead];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) id[u] = i + u * threads < len ? history[i + u * threads] : 0;
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      if (i + u * threads < len) note_token(id[u], i + u * threads);
-  }
-  if (draft) {
-    for (int64_t i = tid; i < a.draft_first; i += threads) {
-      const int64_t id = draft[i];
-      const uint64_t l = (uint64_t)(id - c0);
-      if (l < (uint64_t)n) Cells<C>::add(count, (int)l);
-      if (id >= a.vocab) bad = true;
-    }
-  }
-  if (tid < a.bias_count) note_bias(first_bias, tid);
-  for (int64_t i = tid + threads; i < a.bias_count; i += threads) note_bias(bias_ids[i], i);
-  __syncthreads();
-  // A thread looks at 32 ids and keeps their bits; the warp then takes its
-  // places in the list at once.
-  for (int w0 = (tid >> 5) * 32; w0 < words; w0 += threads) {
-    const int w = w0 + lane;
-    uint32_t word = 0u;
-    if (w < words) {
-      word = in_prompt[w];
-      constexpr int kPer = 16 / sizeof(C);  // cells of 16 bytes
-      auto look = [&](const C* cells) {
-#pragma unroll
-        for (int i = 0; i < 32 / kPer; ++i) {
-          const uint4 x = *reinterpret_cast<const uint4*>(cells + w * 32 + i * kPer);
-          if (x.x | x.y | x.z | x.w) {
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) {
-              const uint32_t v = sizeof(C) == 4 ? (e == 0 ? x.x : e == 1 ? x.y : e == 2 ? x.z : x.w)
-                                                : ((e < 2 ? x.x : e < 4 ? x.y : e < 6 ? x.z : x.w) >> (16 * (e & 1))) & 0xffffu;
-              if (v) word |= 1u << (i * kPer + e);
-            }
-          }
-        }
-      };
-      look(count);
-      if (p.has_bias) look(slot);
-      touched[w] = word;
-    }
-    const int mine = __popc(word);
-    int sum = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int before = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += before;
-    }
-    int base = 0;
-    if (lane == 31 && sum) base = atomicAdd(&listed_count, sum);
-    base = __shfl_sync(0xffffffffu, base, 31) + sum - mine;
-    for (; word; word &= word - 1u) list[base++] = (uint16_t)(w * 32 + __ffs((int)word) - 1);
-  }
+  // What is listed in the stretch: a run of entries in each part that it meets.
+  for (int i = tid; i < words; i += threads) touched[i] = 0u;
   const float rho = a.repetition ? a.repetition[b] : a.repetition_value;
   const float freq = a.frequency ? a.frequency[b] : a.frequency_value;
   const float pres = a.presence ? a.presence[b] : a.presence_value;
-  const float* bias = a.bias_values + b * a.bias_stride;
+  const int64_t* draft = a.draft ? a.draft + b * a.draft_stride + a.draft_first : nullptr;
+  const int blocks = p.parts ? p.part / kBlock : 1, block0 = (int)(c0 / kBlock), block1 = (int)((c0 + n + kBlock - 1) / kBlock);
+  const int part0 = block0 / blocks, part1 = p.parts ? (block1 - 1) / blocks + 1 : part0;
+  auto run = [&](int part, int64_t* from, int64_t* to) {
+    const int64_t which = b * p.parts + part;
+    const uint32_t* before = plane<uint32_t>(a, p.before) + which * (blocks + 1);
+    *from = which * p.entries + before[max(block0 - part * blocks, 0)];
+    *to = which * p.entries + before[min(block1 - part * blocks, blocks)];
+  };
+  const uint32_t* ids = plane<uint32_t>(a, p.ids);
+  const uint32_t* counts = plane<uint32_t>(a, p.counts);
+  const float* biases = plane<float>(a, p.biases);
   __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the lists are there
+  if (keyed) {
+    for (int part = part0; part < part1; ++part) {
+      int64_t from, to;
+      run(part, &from, &to);
+      for (int64_t e = from + tid; e < to; e += threads) {
+        const int l = (int)((int64_t)(ids[e] & ~kFlag) - c0);
+        atomicOr(&touched[l >> 5], 1u << (l & 31));
+      }
+    }
+    __syncthreads();
+  }
 
   for (int64_t k0 = 0; k0 < rows; k0 += kRows) {
     const int group = (int)min((int64_t)kRows, rows - k0);
-    // The last rows' drafted tokens join the counts. Those of these rows are
-    // laid out and listed, which changes nothing for rows before them.
-    if (draft && tid == 0) {
-      for (int q = 0; k0 > 0 && q < kRows; ++q)
-        if (drafted[q] >= 0) count[drafted[q]] += 1;
-      for (int q = 0; q < kRows; ++q) {
-        const int64_t id = k0 + q < rows - 1 ? draft[a.draft_first + k0 + q] : -1;
-        if (id >= a.vocab) bad = true;
-        const int64_t l = id - c0;
-        const bool here = id >= 0 && l >= 0 && l < n;
-        drafted[q] = here ? (int)l : -1;
-        if (here && !bit(touched, (int)l)) {
-          touched[l >> 5] |= 1u << (l & 31);
-          list[listed_count++] = (uint16_t)l;
-        }
-      }
+    if (tid < kRows) {
+      listed_key[tid] = 0ull;
+      const int64_t id = draft && k0 + tid < rows - 1 ? draft[k0 + tid] : -1;
+      drafted[tid] = id >= 0 && id < a.vocab ? (int)id : -1;
     }
-    if (tid < kRows) listed_key[tid] = 0ull;
-    __syncthreads();
-
     const T* in = in0 + k0 * a.in_row;
     T* out = out0 + k0 * a.out_row;
     const uint32_t* mask = mask0 ? mask0 + k0 * a.allowed_row : nullptr;
@@ -383,7 +476,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) constrain_kernel(ConstrainArgs
     auto single = [&](int64_t k, int l) {
       const T y = !mask || bit(mask, l) ? in[l] : from_f32<T>(-INFINITY);
       out[l] = y;
-      if (!a.keys || bit(touched, l)) return;
+      if (!keyed || bit(touched, l)) return;
       if (!a.greedy) {
         key = max_key(key, score(to_f32(y), k, l));
       } else if (better(to_f32(y))) {
@@ -406,7 +499,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) constrain_kernel(ConstrainArgs
             raw = Vec<T>::masked(raw, ALIGNED ? ahead[u].lo >> (l & 31)
                                               : __funnelshift_r(ahead[u].lo, ahead[u].hi, l & 31));
           __stcs(reinterpret_cast<uint4*>(out + head) + j, raw);
-          if (a.keys) {
+          if (keyed) {
             raw = Vec<T>::masked(raw, ~bits_at<ALIGNED>(touched, l, words - 1));
             if (a.greedy) {
               const float top = Vec<T>::max_of(raw);
@@ -426,7 +519,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) constrain_kernel(ConstrainArgs
         j += threads;
         if (--q == 0) {
           for (int t = head + (n - head) / kE * kE + tid; t < n; t += threads) single(k0 + r, t);
-          if (a.keys) {
+          if (keyed) {
             if (a.greedy && best_at >= 0) {
               if (!best_single) {
                 int first = kE;
@@ -462,141 +555,195 @@ __global__ void __launch_bounds__(kMaxThreads, 2) constrain_kernel(ConstrainArgs
 
     // The listed logits of these rows, after the copies of them. What the copy
     // left in place of a masked one stays; in place, an allowed one's input is
-    // what the copy wrote.
-    const int listed = listed_count, items = listed * group;
-    for (int i0 = tid; i0 < items; i0 += threads * kListed) {
-      T x[kListed];
-      uint32_t word[kListed];
+    // what the copy wrote. A step takes EN entries and RN of their rows.
+    auto listed = [&](auto entries_per_step, auto rows_per_step) {
+      constexpr int EN = decltype(entries_per_step)::value, RN = decltype(rows_per_step)::value;
+      for (int part = part0; part < part1; ++part) {
+        int64_t from, to;
+        run(part, &from, &to);
+        for (int64_t e0 = from + tid; e0 < to; e0 += threads * EN) {
+          uint32_t id[EN], counted[EN];
 #pragma unroll
-      for (int u = 0; u < kListed; ++u) {
-        const int item = min(i0 + u * threads, items - 1), g = item / listed;
-        const int64_t k = k0 + g;
-        const int l = (int)list[item - g * listed];
-        x[u] = in0[k * a.in_row + l];
-        word[u] = mask0 ? mask0[k * a.allowed_row + (l >> 5)] : ~0u;
-      }
+          for (int u = 0; u < EN; ++u) {
+            const int64_t e = min(e0 + u * threads, to - 1);
+            id[u] = ids[e];
+            counted[u] = counts[e];
+          }
+          if (draft && k0 > 0) {  // drafted in earlier groups
+            for (int64_t d = 0; d < k0; ++d) {
+              const int64_t t = draft[d];
 #pragma unroll
-      for (int u = 0; u < kListed; ++u) {
-        const int item = i0 + u * threads;
-        if (item >= items) break;
-        const int g = item / listed;
-        const int64_t k = k0 + g;
-        const int l = (int)list[item - g * listed];
-        if (!((word[u] >> (l & 31)) & 1u)) continue;
-        uint32_t times = (uint32_t)count[l];
-        if (draft) {
+              for (int u = 0; u < EN; ++u) counted[u] += t == (int64_t)(id[u] & ~kFlag) ? 1u : 0u;
+            }
+          }
+          for (int g0 = 0; g0 < group; g0 += RN) {
+            T x[EN][RN];
+            uint32_t word[EN][RN];
 #pragma unroll
-          for (int d = 0; d < kRows - 1; ++d) times += d < g && drafted[d] == l ? 1u : 0u;
+            for (int u = 0; u < EN; ++u)
+#pragma unroll
+              for (int g = 0; g < RN; ++g) {
+                const int l = (int)((int64_t)(id[u] & ~kFlag) - c0);
+                const int64_t k = k0 + min(g0 + g, group - 1);
+                x[u][g] = in0[k * a.in_row + l];
+                word[u][g] = mask0 ? mask0[k * a.allowed_row + (l >> 5)] : ~0u;
+              }
+#pragma unroll
+            for (int u = 0; u < EN; ++u) {
+              const float beta = (id[u] & kFlag) ? biases[min(e0 + u * threads, to - 1)] : 0.0f;
+#pragma unroll
+              for (int g = 0; g < RN; ++g) {
+                const int l = (int)((int64_t)(id[u] & ~kFlag) - c0), row = g0 + g;
+                if (row >= group || e0 + u * threads >= to) break;
+                const uint32_t times = counted[u] & ~kFlag;
+                if (drafted[row] == (int)(id[u] & ~kFlag)) counted[u] += 1u;  // from the next row on
+                if (!((word[u][g] >> (l & 31)) & 1u)) continue;
+                float f = to_f32(x[u][g]);
+                if (times || ((counted[u] & kFlag) != 0u)) f = f > 0.0f ? __fdiv_rn(f, rho) : __fmul_rn(f, rho);
+                if (times) f = __fsub_rn(__fsub_rn(f, __fmul_rn(freq, (float)times)), pres);
+                if (id[u] & kFlag) f = __fadd_rn(f, beta);
+                const T y = from_f32<T>(f);
+                out0[(k0 + row) * a.out_row + l] = y;
+                if (keyed) {
+                  const unsigned long long own =
+                      a.greedy ? pack_key(to_f32(y), (uint32_t)(c0 + l)) : score(to_f32(y), k0 + row, l);
+                  if (own > *reinterpret_cast<volatile unsigned long long*>(&listed_key[row]))
+                    atomicMax(&listed_key[row], own);
+                }
+              }
+            }
+          }
         }
-        float f = to_f32(x[u]);
-        if (times || bit(in_prompt, l)) f = f > 0.0f ? __fdiv_rn(f, rho) : __fmul_rn(f, rho);
-        if (times) f = __fsub_rn(__fsub_rn(f, __fmul_rn(freq, (float)times)), pres);
-        if (p.has_bias && slot[l]) f = __fadd_rn(f, bias[(uint32_t)slot[l] - 1u]);
-        const T y = from_f32<T>(f);
-        out0[k * a.out_row + l] = y;
-        if (a.keys) {
-          const unsigned long long mine = a.greedy ? pack_key(to_f32(y), (uint32_t)(c0 + l)) : score(to_f32(y), k, l);
-          if (mine > *reinterpret_cast<volatile unsigned long long*>(&listed_key[g])) atomicMax(&listed_key[g], mine);
-        }
       }
-    }
+    };
+    if (group >= 3)
+      listed(Int<1>{}, Int<kInFlight>{});
+    else
+      listed(Int<kInFlight>{}, Int<1>{});
     __syncthreads();
-    if (a.keys && tid < group) {
+    if (keyed && tid < group) {
       unsigned long long top = listed_key[tid];
       for (int w = 0; w < threads / 32; ++w) top = max_key(top, warp_key[tid][w]);
-      a.keys[(b * rows + k0 + tid) * p.stretches + stretch] = top;
+      atomicMax(plane<unsigned long long>(a, 0) + b * rows + k0 + tid, top);
+      __threadfence();
     }
   }
-  if (bad) report_status(a.status, DSPARK_STATUS_TOKEN_RANGE);
-}
-
-// The token of each row: the id in the largest of its stretches' keys.
-__global__ void __launch_bounds__(32) choose_kernel(ConstrainArgs a, int stretches) {
-  const int64_t row = blockIdx.x;
-  unsigned long long best = 0ull;
-  for (int i = threadIdx.x; i < stretches; i += 32) best = max_key(best, a.keys[row * stretches + i]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) best = max_key(best, __shfl_xor_sync(0xffffffffu, best, o));
-  if (threadIdx.x == 0) a.tokens[row / a.block * a.tokens_batch + row % a.block] = (int64_t)key_token(best);
-}
-
-// The stretches for which the waves of CTAs take least. A CTA's cost, in ids:
-// its own ids for each row and once for the state, and a fixed part for its
-// start and the history, which all CTAs of a sequence read whole. CTAs that
-// share an SM share its rate.
-ConstrainPlan plan_constrain(const ConstrainArgs& a, int width, int num_sms) {
-  ConstrainPlan best{};
-  best.has_bias = a.bias_count > 0 ? 1 : 0;
-  int64_t best_cost = INT64_MAX;
-  const int64_t fixed = 4096 + (a.history ? a.history_cap / 4 : 0), passes = std::min<int64_t>(a.block, 1024) + 1;
-  const auto consider = [&](int64_t stretches) {
-    const int64_t least = (a.vocab + kMaxStretch - 1) / kMaxStretch;
-    stretches = std::max<int64_t>(least, std::min<int64_t>(stretches, (a.vocab + kMinStretch - 1) / kMinStretch));
-    const int64_t stretch = ((a.vocab + stretches - 1) / stretches + kMinStretch - 1) / kMinStretch * kMinStretch;
-    const int64_t real = (a.vocab + stretch - 1) / stretch;
-    const int64_t bytes = state_bytes(stretch, width, best.has_bias != 0);
-    if (bytes > kSmem) return;
-    const int64_t threads = std::min<int64_t>(kMaxThreads, std::max<int64_t>(64, stretch / 16)) / 32 * 32;
-    const int64_t per_sm = std::min<int64_t>(1024 / threads, (227 * 1024) / (bytes + 2304));
-    const int64_t waves = (a.batch * real + per_sm * num_sms - 1) / (per_sm * num_sms);
-    const int64_t shared = std::min(per_sm, (a.batch * real + num_sms - 1) / num_sms);
-    const int64_t cost = waves * shared * (fixed + stretch * passes);
-    if (cost < best_cost) {
-      best_cost = cost;
-      best.stretch = (int)stretch;
-      best.stretches = (int)real;
-      best.threads = (int)threads;
+  // The last CTA of a sequence has all its keys; their ids are the tokens.
+  if (keyed) {
+    __syncthreads();
+    if (tid == 0) {
+      __threadfence();
+      last = atomicAdd(plane<uint32_t>(a, p.counters) + b, 1u) == (uint32_t)p.stretches - 1u;
+      __threadfence();
     }
-  };
-  for (int64_t ctas = 1; ctas <= 8; ++ctas) consider(ctas * num_sms / a.batch);  // per SM, in all
-  consider((a.vocab + kMaxStretch / 4 - 1) / (kMaxStretch / 4));
-  return best;
+    __syncthreads();
+    if (last)
+      for (int64_t k = tid; k < rows; k += threads)
+        a.tokens[b * a.tokens_batch + k] = (int64_t)key_token(__ldcg(plane<unsigned long long>(a, 0) + b * rows + k));
+  }
 }
 
-template <typename T, typename C>
-cudaError_t launch_typed(const ConstrainArgs& a, int num_sms, cudaStream_t s, ConstrainPlan* plan) {
+int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+
+// The plan goes by sizes alone, so that a caller can make the scratch anywhere.
+ConstrainPlan plan_constrain(const ConstrainArgs& a) {
+  constexpr int64_t num_sms = 148;
+  ConstrainPlan p{};
+  p.has_bias = a.bias_count > 0 ? 1 : 0;
+  const int64_t tokens = (a.history ? a.history_cap : 0) + a.draft_most;
+  p.narrow = tokens <= 0xffff && a.bias_count <= 0xfffe ? 1 : 0;
+  const int64_t vocab = round_up(a.vocab, kBlock);
+  if (tokens + a.bias_count > 0 || a.tokens) {
+    // Parts: as few as shared memory allows, since each reads the history, but
+    // as many as there are SMs.
+    const int64_t bits_per_id = (p.narrow ? 16 : 32) * (p.has_bias ? 2 : 1) + 2;
+    const int64_t most = std::min<int64_t>(kMaxPart, (int64_t)kListSmem * 8 / bits_per_id) / kBlock * kBlock;
+    int64_t parts = (vocab + most - 1) / most;
+    parts = std::max(parts, std::min(num_sms / a.batch, vocab / (2 * kBlock)));
+    p.part = (int)round_up((vocab + parts - 1) / parts, kBlock);
+    p.parts = (int)((vocab + p.part - 1) / p.part);
+    p.list_threads = (int)std::min<int64_t>(kListThreads, std::max<int64_t>(256, round_up(p.part / 32, 32)));
+  }
+  // Stretches: two CTAs of 512 threads per SM, in whole waves, each with at
+  // least a few vectors per thread; smaller ones where rows are few.
+  const int64_t slots = 2 * num_sms;
+  int64_t stretch = kMaxStretch;
+  for (int64_t waves = 1; waves <= 8; ++waves) {
+    const int64_t each = std::max<int64_t>(1, waves * slots / a.batch);  // stretches of a sequence
+    stretch = round_up((vocab + each - 1) / each, kBlock);
+    if (stretch <= 16384) break;
+  }
+  if (stretch > 16384) stretch = 16384;
+  p.stretch = (int)stretch;
+  p.stretches = (int)((a.vocab + stretch - 1) / stretch);
+  p.copy_threads = (int)std::min<int64_t>(kCopyThreads, std::max<int64_t>(64, stretch / 16 / 32 * 32));
+
+  p.entries = std::min<int64_t>(p.part, tokens + a.bias_count);
+  const int64_t lists = a.batch * p.parts;
+  int64_t at = round_up(a.tokens ? a.batch * a.block * 8 : 0, 16);
+  const auto take = [&at](int64_t bytes) {
+    const int64_t from = at;
+    at = round_up(at + bytes, 16);
+    return from;
+  };
+  p.counters = take(a.tokens ? a.batch * 4 : 0);
+  p.before = take(p.parts ? lists * (p.part / kBlock + 1) * 4 : 0);
+  p.ids = take(lists * p.entries * 4);
+  p.counts = take(lists * p.entries * 4);
+  p.biases = take(p.has_bias ? lists * p.entries * 4 : 0);
+  p.bytes = at;
+  return p;
+}
+
+template <typename C>
+cudaError_t launch_list(const ConstrainArgs& a, const ConstrainPlan& p, cudaStream_t s) {
+  const size_t bytes = (size_t)p.part / 8 * 2 + (size_t)p.part * sizeof(C) * (p.has_bias ? 2 : 1);
+  if (bytes > 40 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(list_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, kListSmem);
+    if (e != cudaSuccess) return e;
+  }
+  list_kernel<C><<<(unsigned)(a.batch * p.parts), p.list_threads, bytes, s>>>(a, p);
+  note_launch();
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_copy(const ConstrainArgs& a, const ConstrainPlan& p, cudaStream_t s) {
   const auto whole = [&a](const void* base, int64_t batch, int64_t row) {
     constexpr int64_t kE = Vec<T>::kE;
     return reinterpret_cast<uintptr_t>(base) % 16 == 0 && (a.batch == 1 || batch % kE == 0) &&
            (a.block == 1 || row % kE == 0);
   };
   const bool aligned = whole(a.in, a.in_batch, a.in_row) && whole(a.out, a.out_batch, a.out_row);
-  auto kernel = aligned ? constrain_kernel<T, C, true> : constrain_kernel<T, C, false>;
-  const ConstrainPlan p = plan_constrain(a, (int)sizeof(C), num_sms);
-  *plan = p;
-  if (a.batch * p.stretches > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  const size_t bytes = (size_t)state_bytes(p.stretch, (int)sizeof(C), p.has_bias != 0);
-  if (bytes > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-  }
-  kernel<<<(unsigned)(a.batch * p.stretches), p.threads, bytes, s>>>(a, p);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(a.batch * p.stretches));
+  cfg.blockDim = dim3((unsigned)p.copy_threads);
+  cfg.dynamicSmemBytes = (size_t)p.stretch / 8;
+  cfg.stream = s;
+  // Starts while the lists are made; its first loads do not need them.
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = p.parts ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, aligned ? copy_kernel<T, true> : copy_kernel<T, false>, a, p);
   note_launch();
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace
 
-int64_t constrain_key_count(int64_t batch, int64_t block, int64_t vocab) {
-  return batch * block * ((vocab + kMinStretch - 1) / kMinStretch);
-}
+int64_t constrain_scratch_bytes(const ConstrainArgs& a) { return plan_constrain(a).bytes; }
 
-cudaError_t launch_constrain(const ConstrainArgs& a, int logits_dtype, int num_sms, cudaStream_t s) {
-  if (a.batch * a.block > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  // The most that one id can count, and the largest bias entry.
-  const int64_t most = (a.history ? a.history_cap : 0) + a.draft_first + a.block;
-  const bool narrow = most <= 0xffff && a.bias_count <= 0xfffe;
-  ConstrainPlan p{};
-  cudaError_t e;
-  if (logits_dtype == DSPARK_DTYPE_FP32)
-    e = narrow ? launch_typed<float, uint16_t>(a, num_sms, s, &p) : launch_typed<float, uint32_t>(a, num_sms, s, &p);
-  else
-    e = narrow ? launch_typed<__nv_bfloat16, uint16_t>(a, num_sms, s, &p)
-               : launch_typed<__nv_bfloat16, uint32_t>(a, num_sms, s, &p);
-  if (e != cudaSuccess || !a.keys) return e;
-  choose_kernel<<<(unsigned)(a.batch * a.block), 32, 0, s>>>(a, p.stretches);
-  note_launch();
-  return cudaGetLastError();
+cudaError_t launch_constrain(const ConstrainArgs& a, int logits_dtype, cudaStream_t s) {
+  const ConstrainPlan p = plan_constrain(a);
+  if (a.batch * std::max(p.parts, p.stretches) > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  if (p.parts) {
+    const cudaError_t e = p.narrow ? launch_list<uint16_t>(a, p, s) : launch_list<uint32_t>(a, p, s);
+    if (e != cudaSuccess) return e;
+  }
+  return logits_dtype == DSPARK_DTYPE_FP32 ? launch_copy<float>(a, p, s) : launch_copy<__nv_bfloat16>(a, p, s);
 }
 
 }  // namespace dspark

@@ -167,19 +167,20 @@ struct ConstrainArgs {
   int64_t bias_count, bias_stride;
   const int64_t* draft;  // drafted tokens [batch, ...]; row k follows the first draft_first + k of them
   int64_t draft_stride, draft_first;
+  int64_t draft_most;  // drafted tokens that the scratch is made for: draft_first + block - 1 at least, 0 without draft
   const uint32_t* allowed;  // bit v of a row's words, or null
   int64_t allowed_batch, allowed_row;
-  unsigned long long* keys;  // scratch of constrain_key_count() keys, or null: no tokens wanted
-  int64_t* tokens;
+  void* scratch;   // constrain_scratch_bytes() of it
+  int64_t* tokens; // or null: none wanted
   int64_t tokens_batch;  // the token of row (b, k) at tokens[b * tokens_batch + k]
   int32_t greedy;
   float temperature;
   uint64_t seed;
   uint32_t* status;
 };
-// Upper bound of the keys that a call of these sizes uses.
-int64_t constrain_key_count(int64_t batch, int64_t block, int64_t vocab);
-cudaError_t launch_constrain(const ConstrainArgs& a, int logits_dtype, int num_sms, cudaStream_t s);
+// Of the arguments only the sizes matter, and which pointers are null.
+int64_t constrain_scratch_bytes(const ConstrainArgs& a);
+cudaError_t launch_constrain(const ConstrainArgs& a, int logits_dtype, cudaStream_t s);
 
 // The training loss and its gradient (loss.cu).
 struct LossArgs {

@@ -361,8 +361,7 @@ class VanillaMarkov:
         if batch == 0:
             return tokens, corrected
         with _device_guard(self.device):
-            scratch = torch.empty(self._lib.dspark_markov_constrain_scratch_bytes(batch, 1, vocab),
-                                  dtype=torch.uint8, device=self.device)
+            scratch = constraints._scratch(self.device, batch, 1, m, True)
             code = self._lib.dspark_markov_sample_block_constrained(
                 base_logits.data_ptr(), prev.data_ptr(), batch, m, vocab, self.markov_w1.data_ptr(),
                 self.markov_w2.data_ptr(), self.markov_rank, temperature, seed & 0xFFFFFFFFFFFFFFFF, constraints._ref,

@@ -114,12 +114,12 @@ def test_c_entry_refusals(lib):
 
     assert process(b=0) == ok and process(m=0) == ok
     assert process(b=-1) == bad and process(v=0) == bad and process(dt=2) == bad and process(con=None) == bad
-    assert process(x=None) == bad and process(out=None) == bad and process(tok=p) == bad  # tokens without scratch
+    assert process(x=None) == bad and process(out=None) == bad
     assert process(temp=float("nan")) == bad and process(ib=-1) == bad and process(first=-1) == bad
     assert process(ob=100) == bad and process(orow=63) == bad and process(ob=0) == bad  # rows that overlap
     assert process(out=p, orow=64, ob=200) == bad  # in place with other strides
     assert process(out=ctypes.c_void_p((1 << 20) + 256)) == bad  # another overlap
-    assert process(x=ctypes.c_void_p((1 << 20) + 2)) == bad and process(scratch=ctypes.c_void_p(4)) == bad
+    assert process(x=ctypes.c_void_p((1 << 20) + 2)) == bad and process(scratch=ctypes.c_void_p(8)) == bad
     assert process(tok=p, scratch=far, ts=2) == bad and process(draft=p, ds=1) == bad
     assert process(v=1 << 33, ib=0, ir=0, ob=1 << 40, orow=1 << 35) == N.DSPARK_ERR_UNSUPPORTED
     assert process(b=1 << 20, m=1 << 20) == N.DSPARK_ERR_UNSUPPORTED
@@ -128,7 +128,11 @@ def test_c_entry_refusals(lib):
         setattr(d, field, value)
         assert process(con=ctypes.byref(d)) == bad, field
     size = lib.dspark_markov_constrain_scratch_bytes
-    assert size(2, 3, 64) >= 48 and size(0, 3, 64) == 0 and size(2, 3, 0) == 0 and size(1 << 20, 1 << 20, 64) == 0
+    assert size(2, 3, 64, 0, 0, 0, 1) >= 48 and size(2, 3, 64, 0, 0, 0, 0) == 0
+    assert size(2, 3, 64, 100, 0, 0, 0) >= 2 * 64 * 8 and size(2, 3, 64, 100, 5, 2, 1) > size(2, 3, 64, 100, 0, 2, 1)
+    for refused in ((0, 3, 64, 0, 0, 0, 1), (2, 3, 0, 0, 0, 0, 1), (1 << 20, 1 << 20, 64, 0, 0, 0, 1),
+                    (2, 3, 1 << 31, 0, 0, 0, 1), (2, 3, 64, 1 << 30, 0, 0, 1), (2, 3, 64, -1, 0, 0, 1)):
+        assert size(*refused) == 0
     sm = lib.dspark_markov_sample_block_constrained
 
     def sample(base=p, out=far, b=2, m=3, rank=16, temp=0.0, con=ref, scratch=far, ldt=0):

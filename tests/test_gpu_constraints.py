@@ -145,6 +145,9 @@ SHAPES = [  # batch, block, vocab, history, biases, mask
     (1, 2, 151936, 40000, 64, "rows"),
     (40, 0, 2056, 2, 0, "rows"),
     (3, 1, 9001, 33000, 2, None),
+    (1, 2, 5000, 70000, 3, None),
+    (2, 3, 3001, 4, 70000, "rows"),
+    (1, 19, 2500, 9, 2, "rows"),
 ]
 
 
