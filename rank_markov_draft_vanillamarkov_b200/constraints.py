@@ -224,5 +224,6 @@ def process_logits(logits: torch.Tensor, constraints: TokenConstraints, *,
             ostride[0], ostride[1] if dim == 3 else vocab, constraints._ref, draft, block, 0, mask, mask_batch,
             mask_row, tokens.data_ptr() if tokens is not None else None, block, 0.0, 0,
             scratch.data_ptr() if scratch is not None else None, _DT[dtype], _stream_ptr(device))
-    N.check(code, "dspark_markov_process_logits")
+    if code:
+        N.check(code, "dspark_markov_process_logits")
     return out, tokens

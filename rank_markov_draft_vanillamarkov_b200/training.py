@@ -70,12 +70,13 @@ def block_cross_entropy(logits: torch.Tensor, targets: torch.Tensor, *, weights:
     lib = N.load()
     with _device_guard(device):
         loss = torch.empty((), dtype=torch.float32, device=device)
-        row_losses = torch.empty(lead, dtype=torch.float32, device=device)
+        row_losses = torch.empty_like(ids, dtype=torch.float32)
         code = lib.dspark_markov_block_cross_entropy(
             logits.data_ptr(), ids.data_ptr(), weights.data_ptr() if weights is not None else None, rows, vocab,
             ignore_index, reduction == "mean", loss.data_ptr(), row_losses.data_ptr(),
             grad.data_ptr() if grad is not None else None, _DT[dtype], _stream_ptr(device))
-    N.check(code, "dspark_markov_block_cross_entropy")
+    if code:
+        N.check(code, "dspark_markov_block_cross_entropy")
     return loss, row_losses, grad
 
 
@@ -89,7 +90,9 @@ class GradientClipper:
     clipped gradients (each its gradient itself or memory that overlaps none of
     them); None: in place. Creating the object lays the tensors out as a plan
     in device memory (a host-to-device copy: create it before a graph capture);
-    ``clip`` reads what the tensors hold at each call.
+    ``clip`` reads what the tensors hold at each call. Calls of one object are
+    ordered on one stream or by events, as anything that writes the same
+    tensors is.
     """
 
     def __init__(self, grads: Sequence[torch.Tensor], *, out: Optional[Sequence[torch.Tensor]] = None):
@@ -117,6 +120,10 @@ class GradientClipper:
         plan = (N.ClipPiece * max(1, self._pieces))()
         self._checked(lib.dspark_markov_clip_plan(*args, plan, self._pieces, ctypes.byref(pieces)))
         self._plan = torch.frombuffer(plan, dtype=torch.uint8).to(self.device)
+        # Calls of one object write one set of outputs, so they are ordered and can share this.
+        self._work = torch.empty(N.DSPARK_CLIP_SCRATCH_BYTES, dtype=torch.uint8, device=self.device)
+        self._call = lib.dspark_markov_clip_grad_norm
+        self._fixed = (self._plan.data_ptr(), self._work.data_ptr())
 
     @staticmethod
     def _checked(code: int) -> None:
@@ -133,12 +140,12 @@ class GradientClipper:
         if math.isnan(max_norm) or max_norm < 0.0:
             raise ValueError("max_norm must not be negative or NaN")
         device = self.device
+        plan, work = self._fixed
         with _device_guard(device):
             norm = torch.empty((), dtype=torch.float32, device=device)
-            scratch = torch.empty(N.DSPARK_CLIP_SCRATCH_BYTES, dtype=torch.uint8, device=device)
-            code = N.load().dspark_markov_clip_grad_norm(self._plan.data_ptr(), self._pieces, max_norm,
-                                                         norm.data_ptr(), scratch.data_ptr(), _stream_ptr(device))
-        N.check(code, "dspark_markov_clip_grad_norm")
+            code = self._call(plan, self._pieces, max_norm, norm.data_ptr(), work, _stream_ptr(device))
+        if code:
+            N.check(code, "dspark_markov_clip_grad_norm")
         return norm
 
 
