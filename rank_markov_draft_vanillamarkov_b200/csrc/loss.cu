@@ -18,6 +18,7 @@
 // with the next row's chunk.
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -30,6 +31,7 @@ namespace {
 constexpr int kMaxThreads = 512;  // that compute; one warp more issues the copies
 constexpr int kMaxWarps = kMaxThreads / 32;
 constexpr int kMaxCluster = 16;
+constexpr int kWholeCtas = 8;   // of a launch that is one cluster
 constexpr int kMaxSlots = 8;
 constexpr int kRing = 222 * 1024;  // bytes, at most; the barriers and pairs take 4.4 KB more
 constexpr int kPerThread = 4;  // vectors of a chunk for each thread, at most
@@ -173,6 +175,25 @@ struct RowShape {
   __device__ __forceinline__ int edge(int k) const { return k < head ? k : k + vecs * Vectors<T>::kE; }
 };
 
+// loss = sum_i w_i nll_i / N over the live rows, and the status of the targets,
+// by one CTA.
+__device__ void sum_loss(const LossArgs& a, double* sums) {
+  const double inv_n = inverse_total(a, sums, true);
+  double s = 0.0;
+  for (int64_t i = threadIdx.x; i < a.rows; i += blockDim.x) {
+    int64_t t;
+    float w;
+    if (live_row(a, i, &t, &w)) s += (double)w * (double)__ldcg(a.row_losses + i);
+  }
+  s = block_sum(s, sums);
+  if (threadIdx.x == 0) *a.loss = (float)(s * inv_n);
+}
+__global__ void __launch_bounds__(kMaxThreads) loss_sum_kernel(LossArgs a) {
+  __shared__ double sums[kMaxWarps + 1];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  sum_loss(a, sums);
+}
+
 struct LossPlan {
   int cluster;  // CTAs per row
   int warps;    // that compute, per CTA
@@ -180,6 +201,7 @@ struct LossPlan {
   int chunk;    // vectors per chunk, at most 32 kPerThread warps
   int chunks;   // chunks per slice
   int slots;    // chunks in the ring, at least `chunks`
+  int whole;    // the launch is one hardware cluster, a CTA per row, which also sums the loss
 };
 
 struct RowBarriers {
@@ -209,12 +231,13 @@ __global__ void __launch_bounds__(kMaxThreads + 32, 1) loss_rows_kernel(LossArgs
   __shared__ double sums[kMaxWarps + 1];
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = (int)threadIdx.x;
-  const int ranks = p.cluster, rank = (int)cluster_rank(), warps = p.warps, threads = warps * 32;
+  const int ranks = p.cluster, rank = ranks > 1 ? (int)cluster_rank() : 0, warps = p.warps, threads = warps * 32;
   const int64_t step = gridDim.x / ranks, first = blockIdx.x / ranks;
   const int vocab = (int)a.vocab;
   const T* logits = static_cast<const T*>(a.logits);
   T* grads = static_cast<T*>(a.grad);
   const WaitCtl ctl{&abort_flag, a.status, a.wait_limit_ns};
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // The next live row at or after i.
   auto seek = [&](int64_t i, int64_t* t, float* w) {
     while (i < a.rows && !live_row(a, i, t, w)) i += step;
@@ -460,6 +483,10 @@ __global__ void __launch_bounds__(kMaxThreads + 32, 1) loss_rows_kernel(LossArgs
     __syncwarp();
   }
   if (ranks > 1) cluster_barrier();  // no CTA leaves while others may still send to it
+  if (p.whole) {
+    cluster_barrier();  // every row's loss is written
+    if (blockIdx.x == 0) sum_loss(a, sums);
+  }
 }
 
 // Rows longer than a cluster's shared memory: one CTA per row reads it twice.
@@ -514,20 +541,6 @@ __global__ void __launch_bounds__(kMaxThreads) loss_long_rows_kernel(LossArgs a)
   }
 }
 
-// loss = sum_i w_i nll_i / N over the live rows, and the status of the targets.
-__global__ void __launch_bounds__(kMaxThreads) loss_sum_kernel(LossArgs a) {
-  __shared__ double sums[kMaxWarps + 1];
-  const double inv_n = inverse_total(a, sums, true);
-  double s = 0.0;
-  for (int64_t i = threadIdx.x; i < a.rows; i += blockDim.x) {
-    int64_t t;
-    float w;
-    if (live_row(a, i, &t, &w)) s += (double)w * (double)a.row_losses[i];
-  }
-  s = block_sum(s, sums);
-  if (threadIdx.x == 0) *a.loss = (float)(s * inv_n);
-}
-
 // The cluster and ring for a row of `vecs` vectors, or cluster 0 where none
 // holds it.
 LossPlan plan_loss(int64_t rows, int64_t vecs, int num_sms) {
@@ -537,8 +550,11 @@ LossPlan plan_loss(int64_t rows, int64_t vecs, int num_sms) {
   while (cluster <= kMaxCluster && cluster * kMaxSlice < vecs) cluster *= 2;
   LossPlan p{};
   if (cluster > kMaxCluster) return p;
+  // Small calls: one launch, all rows in one cluster of CTAs with a row each at
+  // a time, instead of a second kernel for the sum.
+  p.whole = cluster == 1 && rows <= 64 && rows * vecs <= 16384 ? 1 : 0;
   // Few rows: more CTAs for each.
-  while (rows * cluster * 2 <= num_sms && cluster < 8 && vecs >= cluster * 2 * 512) cluster *= 2;
+  while (!p.whole && rows * cluster * 2 <= num_sms && cluster < 8 && vecs >= cluster * 2 * 512) cluster *= 2;
   const int64_t slice = std::max<int64_t>(1, (vecs + cluster - 1) / cluster);
   p.cluster = (int)cluster;
   p.slice = (int)slice;
@@ -552,44 +568,73 @@ LossPlan plan_loss(int64_t rows, int64_t vecs, int num_sms) {
   return p;
 }
 
+// How many clusters of a plan run at once on the current device, kept by the
+// plan since asking takes longer than a launch.
 template <typename T, bool SAME>
-cudaError_t launch_rows(const LossArgs& a, const LossPlan& p, int num_sms, cudaStream_t s) {
-  auto kernel = loss_rows_kernel<T, SAME>;
-  cudaLaunchConfig_t cfg{};
-  cfg.blockDim = dim3((unsigned)(p.warps * 32 + 32));
-  cfg.dynamicSmemBytes = (size_t)p.slots * p.chunk * 16;
-  cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim = {(unsigned)p.cluster, 1, 1};
-  cfg.attrs = &attr;
-  cfg.numAttrs = p.cluster > 1 ? 1 : 0;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
-  if (e == cudaSuccess && p.cluster > 8)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+cudaError_t active_clusters(const LossPlan& p, cudaLaunchConfig_t cfg, int num_sms, int* out) {
+  struct Known {
+    int device, cluster, warps;
+    size_t bytes;
+    int clusters;
+  };
+  static std::mutex mu;
+  static Known known[16];
+  static int count = 0;
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return e;
-  // As many clusters as run at once: a persistent grid larger than that would
-  // leave its last clusters, and their rows, to a second wave.
-  cfg.gridDim = dim3((unsigned)p.cluster);
+  std::lock_guard<std::mutex> lock(mu);
+  for (int i = 0; i < std::min(count, 16); ++i)
+    if (known[i].device == device && known[i].cluster == p.cluster && known[i].warps == p.warps &&
+        known[i].bytes == cfg.dynamicSmemBytes) {
+      *out = known[i].clusters;
+      return cudaSuccess;
+    }
+  auto kernel = loss_rows_kernel<T, SAME>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
   int clusters = 0;
   if (p.cluster > 1) {
+    cfg.gridDim = dim3((unsigned)p.cluster);
     e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
   } else {
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&clusters, kernel, (int)cfg.blockDim.x, cfg.dynamicSmemBytes);
     clusters *= num_sms;
   }
   if (e != cudaSuccess) return e;
-  if (clusters < 1) clusters = 1;
-  if (clusters > a.rows) clusters = (int)a.rows;
-  cfg.gridDim = dim3((unsigned)(clusters * p.cluster));
-  e = cudaLaunchKernelEx(&cfg, kernel, a, p);
+  *out = std::max(clusters, 1);
+  known[count++ % 16] = Known{device, p.cluster, p.warps, cfg.dynamicSmemBytes, *out};
+  return cudaSuccess;
+}
+
+template <typename T, bool SAME>
+cudaError_t launch_rows(const LossArgs& a, const LossPlan& p, int num_sms, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.blockDim = dim3((unsigned)(p.warps * 32 + 32));
+  cfg.dynamicSmemBytes = (size_t)p.slots * p.chunk * 16;
+  cfg.stream = s;
+  const int in_cluster = p.whole ? kWholeCtas : p.cluster;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim = {(unsigned)in_cluster, 1, 1};
+  cfg.attrs = &attr;
+  cfg.numAttrs = in_cluster > 1 ? 1 : 0;
+  // As many clusters as run at once: a persistent grid larger than that would
+  // leave its last clusters, and their rows, to a second wave.
+  int clusters = 0;
+  cudaError_t e = active_clusters<T, SAME>(p, cfg, num_sms, &clusters);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)(p.whole ? kWholeCtas : std::min<int64_t>(clusters, a.rows) * p.cluster));
+  e = cudaLaunchKernelEx(&cfg, loss_rows_kernel<T, SAME>, a, p);
   note_launch();
   return e;
 }
 
 template <typename T>
-cudaError_t launch_typed(const LossArgs& a, int num_sms, cudaStream_t s) {
+cudaError_t launch_typed(const LossArgs& a, int num_sms, cudaStream_t s, bool* summed) {
   const LossPlan p = plan_loss(a.rows, a.vocab / Vectors<T>::kE, num_sms);
+  *summed = p.whole != 0;
   if (p.cluster == 0) {
     const int64_t grid = a.rows < 2ll * num_sms ? a.rows : 2ll * num_sms;
     loss_long_rows_kernel<T><<<(unsigned)grid, kMaxThreads, 0, s>>>(a);
@@ -603,14 +648,24 @@ cudaError_t launch_typed(const LossArgs& a, int num_sms, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_loss(const LossArgs& a, int logits_dtype, int num_sms, cudaStream_t s) {
+  bool summed = false;
   if (a.rows > 0) {
-    const cudaError_t e = logits_dtype == DSPARK_DTYPE_FP32 ? launch_typed<float>(a, num_sms, s)
-                                                            : launch_typed<__nv_bfloat16>(a, num_sms, s);
-    if (e != cudaSuccess) return e;
+    const cudaError_t e = logits_dtype == DSPARK_DTYPE_FP32 ? launch_typed<float>(a, num_sms, s, &summed)
+                                                            : launch_typed<__nv_bfloat16>(a, num_sms, s, &summed);
+    if (e != cudaSuccess || summed) return e;
   }
-  loss_sum_kernel<<<1, kMaxThreads, 0, s>>>(a);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(kMaxThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};  // its launch overlaps the rows; it waits for their end
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = a.rows > 0 ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, loss_sum_kernel, a);
   note_launch();
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace dspark
