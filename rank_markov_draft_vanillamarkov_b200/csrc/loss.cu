@@ -12,10 +12,11 @@
 //
 // A CTA's slice of a row lies in a ring of chunks, filled and emptied by bulk
 // copies that one thread issues. Pass 1 walks the chunks as they land, every
-// thread with its own running maximum m and sum s of 2^((c - m) log2 e); the
-// warps' pairs (m, s) meet in every CTA of the cluster. Pass 2 overwrites the
-// chunks by the gradient, each copied out as it is done and its place filled
-// with the next row's chunk.
+// thread with its own running maximum m and sum s of 2^(c log2 e - r), where
+// the reference r = m log2 e is rounded; the warps' pairs (m, s) meet in every
+// CTA of the cluster. Pass 2 overwrites the chunks by the gradient, each copied
+// out as it is done and its place filled with the next row's chunk. All of a
+// row goes by rounded references, so their rounding cancels.
 #include <algorithm>
 #include <cmath>
 #include <mutex>
@@ -34,8 +35,9 @@ constexpr int kMaxCluster = 16;
 constexpr int kWholeCtas = 8;   // of a launch that is one cluster
 constexpr int kMaxSlots = 8;
 constexpr int kRing = 222 * 1024;  // bytes, at most; the barriers and pairs take 4.4 KB more
-constexpr int kPerThread = 4;  // vectors of a chunk for each thread, at most
+constexpr int kPerThread = 4;  // vectors of a chunk for each thread: 4, or 1 in small chunks
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.693147180559945309417f;
 
 // 2^x by the hardware approximation (relative error 2^-22; 0 below 2^-126).
 __device__ __forceinline__ float ex2(float x) {
@@ -44,32 +46,18 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 r;
-  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 x, x, y;\n\t"
-      "mov.b64 {%0, %1}, x;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 r;
-  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 x, x, y;\n\t"
-      "mov.b64 {%0, %1}, x;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
-// exp of x - m for a pair; minus_m holds -m twice.
-__device__ __forceinline__ float2 exp_pair(float2 x, float2 minus_m) {
-  const float2 t = mul2(add2(x, minus_m), make_float2(kLog2e, kLog2e));
-  return make_float2(ex2(t.x), ex2(t.y));
-}
-// The factor that brings a sum with reference m to reference top >= m. A
-// reference of -inf stands for an empty (or NaN) sum, kept as it is.
+// The factor from logits to the exponents' units for logits of which the
+// largest is m. Where m log2 e could overflow, two logits that differ at all do
+// so by far more than any exponent, so a quarter of them serves as well (and
+// stays finite): equal logits have equal exponents, all others vanish.
+__device__ __forceinline__ float unit_for(float m) { return fabsf(m) > 0x1p126f ? 0.25f : kLog2e; }
+__device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.0f : __fmul_rn(m, unit_for(m)); }
+// A sum whose largest logit is m, brought to the reference of top >= m. One
+// without a logit (m = -inf) is zero or NaN and stays; one in other units lies
+// infinitely far below.
 __device__ __forceinline__ float rescaled(float s, float m, float top) {
-  return m == top || m == -INFINITY ? s : s * ex2((m - top) * kLog2e);
+  if (m == top || m == -INFINITY) return s;
+  return unit_for(m) == unit_for(top) ? s * ex2(reference(m) - reference(top)) : s * 0.0f;
 }
 
 // A row counts when its target is not the ignored one, lies in the vocabulary
@@ -112,33 +100,30 @@ __device__ double inverse_total(const LossArgs& a, double* parts, bool report) {
   return s != 0.0 ? 1.0 / s : 0.0;
 }
 
-// 16 bytes of a row, as pairs of fp32.
+// 16 bytes of a row.
 template <typename T>
 struct Vectors;
 template <>
 struct Vectors<float> {
   static constexpr int kE = 4;
   static constexpr uint32_t kFill = 0xff800000u;  // -inf
-  static __device__ __forceinline__ float2 pair(const uint4& r, int i) {
-    return i == 0 ? make_float2(__uint_as_float(r.x), __uint_as_float(r.y))
-                  : make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
+  static __device__ __forceinline__ float get(const uint4& r, int e) {
+    return __uint_as_float(e == 0 ? r.x : e == 1 ? r.y : e == 2 ? r.z : r.w);
   }
   static __device__ __forceinline__ float max_of(const uint4& r) {
-    const float2 a = pair(r, 0), b = pair(r, 1);
-    return fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y));
+    return fmaxf(fmaxf(get(r, 0), get(r, 1)), fmaxf(get(r, 2), get(r, 3)));
   }
-  static __device__ __forceinline__ uint4 pack(const float2* g) {
-    return make_uint4(__float_as_uint(g[0].x), __float_as_uint(g[0].y), __float_as_uint(g[1].x),
-                      __float_as_uint(g[1].y));
+  static __device__ __forceinline__ uint4 pack(const float* g) {
+    return make_uint4(__float_as_uint(g[0]), __float_as_uint(g[1]), __float_as_uint(g[2]), __float_as_uint(g[3]));
   }
 };
 template <>
 struct Vectors<__nv_bfloat16> {
   static constexpr int kE = 8;
   static constexpr uint32_t kFill = 0xff80ff80u;
-  static __device__ __forceinline__ float2 pair(const uint4& r, int i) {
-    const uint32_t w = i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w;
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  static __device__ __forceinline__ float get(const uint4& r, int e) {
+    const uint32_t w = e < 2 ? r.x : e < 4 ? r.y : e < 6 ? r.z : r.w;
+    return __uint_as_float((e & 1) ? (w & 0xffff0000u) : (w << 16));
   }
   static __device__ __forceinline__ __nv_bfloat162 both(uint32_t w) {
     return *reinterpret_cast<const __nv_bfloat162*>(&w);
@@ -147,12 +132,12 @@ struct Vectors<__nv_bfloat16> {
     const __nv_bfloat162 m = __hmax2(__hmax2(both(r.x), both(r.y)), __hmax2(both(r.z), both(r.w)));
     return fmaxf(__low2float(m), __high2float(m));
   }
-  static __device__ __forceinline__ uint32_t pack2(float2 x) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(x.x, x.y);
+  static __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
   }
-  static __device__ __forceinline__ uint4 pack(const float2* g) {
-    return make_uint4(pack2(g[0]), pack2(g[1]), pack2(g[2]), pack2(g[3]));
+  static __device__ __forceinline__ uint4 pack(const float* g) {
+    return make_uint4(pack2(g[0], g[1]), pack2(g[2], g[3]), pack2(g[4], g[5]), pack2(g[6], g[7]));
   }
 };
 
@@ -198,7 +183,8 @@ struct LossPlan {
   int cluster;  // CTAs per row
   int warps;    // that compute, per CTA
   int slice;    // vectors of a row per CTA
-  int chunk;    // vectors per chunk, at most 32 kPerThread warps
+  int chunk;    // vectors per chunk, at most 32 per_thread warps
+  int per_thread;
   int chunks;   // chunks per slice
   int slots;    // chunks in the ring, at least `chunks`
   int whole;    // the launch is one hardware cluster, a CTA per row, which also sums the loss
@@ -222,7 +208,8 @@ __device__ __forceinline__ int slice_vectors(const LossPlan& p, int vecs, int ra
 // SAME: the gradient's rows start at the same offset from a 16-byte address as
 // the logits' (in place, or any vocabulary of whole vectors), so that a chunk
 // is copied out as it was copied in; otherwise gradients are written one by one.
-template <typename T, bool SAME>
+// PT: vectors of a chunk per thread; all but the last exist in every chunk.
+template <typename T, int PT, bool SAME>
 __global__ void __launch_bounds__(kMaxThreads + 32, 1) loss_rows_kernel(LossArgs a, LossPlan p) {
   constexpr int kE = Vectors<T>::kE;
   extern __shared__ __align__(128) uint4 ring[];
@@ -329,15 +316,12 @@ __global__ void __launch_bounds__(kMaxThreads + 32, 1) loss_rows_kernel(LossArgs
     int64_t i = first;
     int64_t t = 0;
     float w = 0.0f;
-    float edge = -INFINITY, xt = 0.0f;  // this thread's edge element; the target's logit (thread 0)
+    float edge = -INFINITY, xt = 0.0f;  // this thread's edge element; the target's logit
     auto load_singles = [&](int64_t row, int64_t target) {
       const T* c = logits + row * vocab;
       const RowShape<T> shape(c, vocab);
-      edge = -INFINITY;
-      if (rank == 0) {
-        if (tid < shape.edges) edge = to_f32(c[shape.edge(tid)]);
-        if (tid == 0) xt = to_f32(c[target]);
-      }
+      edge = rank == 0 && tid < shape.edges ? to_f32(c[shape.edge(tid)]) : -INFINITY;
+      xt = to_f32(c[target]);
     };
     bool live = i < a.rows && live_row(a, i, &t, &w);
     if (live) load_singles(i, t);
@@ -365,30 +349,28 @@ __global__ void __launch_bounds__(kMaxThreads + 32, 1) loss_rows_kernel(LossArgs
       } else {
         // Pass 1. A thread of -inf alone keeps m = -inf and sums zeros (or NaN).
         float m = edge;
-        float s = edge == -INFINITY ? 0.0f : ex2((edge - edge) * kLog2e);
+        float s = edge == -INFINITY ? 0.0f : ex2(fmaf(edge, unit_for(edge), -reference(edge)));
         for (int c = 0; c < p.chunks; ++c) {
           mbar_wait(&bars.full[slot1], phase1, ctl);
           const int n = chunk_vectors(p, count, c);
           const uint4* from = ring + (size_t)slot1 * p.chunk + tid;
-          uint4 raw[kPerThread];
+          uint4 raw[PT];
 #pragma unroll
-          for (int k = 0; k < kPerThread; ++k) {
-            raw[k] = make_uint4(Vectors<T>::kFill, Vectors<T>::kFill, Vectors<T>::kFill, Vectors<T>::kFill);
-            if (tid + k * threads < n) raw[k] = from[k * threads];
-          }
+          for (int k = 0; k < PT - 1; ++k) raw[k] = from[k * threads];
+          raw[PT - 1] = make_uint4(Vectors<T>::kFill, Vectors<T>::kFill, Vectors<T>::kFill, Vectors<T>::kFill);
+          if (tid + (PT - 1) * threads < n) raw[PT - 1] = from[(PT - 1) * threads];
           float top = m;
 #pragma unroll
-          for (int k = 0; k < kPerThread; ++k) top = fmaxf(top, Vectors<T>::max_of(raw[k]));
+          for (int k = 0; k < PT; ++k) top = fmaxf(top, Vectors<T>::max_of(raw[k]));
           s = rescaled(s, m, top);
           m = top;
-          const float minus = top == -INFINITY ? 0.0f : -top;
-          float2 sum[2] = {make_float2(s, 0.0f), make_float2(0.0f, 0.0f)};
+          const float unit = unit_for(top), ref = reference(top);
+          float part[2] = {0.0f, 0.0f};
 #pragma unroll
-          for (int k = 0; k < kPerThread; ++k)
+          for (int k = 0; k < PT; ++k)
 #pragma unroll
-            for (int e = 0; e < kE / 2; ++e)
-              sum[e & 1] = add2(sum[e & 1], exp_pair(Vectors<T>::pair(raw[k], e), make_float2(minus, minus)));
-          s = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            for (int e = 0; e < kE; ++e) part[e & 1] += ex2(fmaf(Vectors<T>::get(raw[k], e), unit, -ref));
+          s += part[0] + part[1];
           if (++slot1 == p.slots) {
             slot1 = 0;
             phase1 ^= 1u;
@@ -428,45 +410,46 @@ __global__ void __launch_bounds__(kMaxThreads + 32, 1) loss_rows_kernel(LossArgs
         parity ^= 1;
         if (parity == 0) met_phase ^= 1u;
         if (isinf(m)) s = NAN;  // +inf somewhere, or -inf everywhere
-        const float scale = (float)((double)w * inv_n), factor = scale / s;
-        if (rank == 0 && tid == 0) a.row_losses[i] = logf(s) + (m - row_xt);
+        const float scale = (float)((double)w * inv_n), factor = scale / s, unit = unit_for(m), ref = reference(m);
+        if (rank == 0 && tid == 0)  // in plain units where the exponents' would overflow
+          a.row_losses[i] = unit == kLog2e && fabsf(row_xt) <= 0x1p126f
+                                ? kLn2 * (log2f(s) - fmaf(row_xt, unit, -ref))
+                                : logf(s) + (m - row_xt);
+        // The gradient at the target, which its owner writes over the rest.
+        const float at_target = ex2(fmaf(row_xt, unit, -ref)) * factor - scale;
         if (g && rank == 0 && tid < shape.edges) {
           const int v = shape.edge(tid);
-          const float e = ex2((row_edge - m) * kLog2e) * factor;
-          g[v] = from_f32<T>(v == (int)t ? e - scale : e);
+          g[v] = from_f32<T>(v == (int)t ? at_target : ex2(fmaf(row_edge, unit, -ref)) * factor);
         }
-        // Pass 2. The target's place in this slice, counted in vectors.
-        const int at = (int)t - shape.head;
-        const int target = at >= 0 ? at / kE - rank * p.slice : -1, te = at % kE;
+        // Pass 2. The target's place in this slice, as chunk and vector, if any.
+        const int at = (int)t - shape.head, vec = at >= 0 ? at / kE - rank * p.slice : -1, te = at % kE;
+        const int tc = vec >= 0 && vec < count ? vec / p.chunk : -1, tj = vec - tc * p.chunk;
+        const bool own_target = tc >= 0 && tj % threads == tid;
         T* to = g + shape.head + (int64_t)rank * p.slice * kE;
         for (int c = 0; c < p.chunks; ++c) {
-          const int n = g ? chunk_vectors(p, count, c) : 0;
+          const int n = chunk_vectors(p, count, c);
           uint4* place = ring + (size_t)slot2 * p.chunk + tid;
+          if (g) {
 #pragma unroll
-          for (int k = 0; k < kPerThread; ++k) {
-            const int j = tid + k * threads;
-            if (j < n) {
+            for (int k = 0; k < PT; ++k) {
+              const int j = tid + k * threads;
+              if (k == PT - 1 && j >= n) break;
               const uint4 raw = place[k * threads];
-              float2 x[kE / 2];
+              float x[kE];
 #pragma unroll
-              for (int e = 0; e < kE / 2; ++e)
-                x[e] = mul2(exp_pair(Vectors<T>::pair(raw, e), make_float2(-m, -m)), make_float2(factor, factor));
-              if (c * p.chunk + j == target) {
-#pragma unroll
-                for (int e = 0; e < kE / 2; ++e) {
-                  if (2 * e == te) x[e].x -= scale;
-                  if (2 * e + 1 == te) x[e].y -= scale;
-                }
-              }
+              for (int e = 0; e < kE; ++e) x[e] = ex2(fmaf(Vectors<T>::get(raw, e), unit, -ref)) * factor;
               if (SAME) {
                 place[k * threads] = Vectors<T>::pack(x);
               } else {
 #pragma unroll
-                for (int e = 0; e < kE / 2; ++e) {
-                  to[((int64_t)c * p.chunk + j) * kE + 2 * e] = from_f32<T>(x[e].x);
-                  to[((int64_t)c * p.chunk + j) * kE + 2 * e + 1] = from_f32<T>(x[e].y);
-                }
+                for (int e = 0; e < kE; ++e) to[((int64_t)c * p.chunk + j) * kE + e] = from_f32<T>(x[e]);
               }
+            }
+            if (own_target && c == tc) {
+              if (SAME)
+                reinterpret_cast<T*>(ring + (size_t)slot2 * p.chunk + tj)[te] = from_f32<T>(at_target);
+              else
+                g[t] = from_f32<T>(at_target);
             }
           }
           if (SAME) fence_proxy_async_smem();
@@ -558,10 +541,13 @@ LossPlan plan_loss(int64_t rows, int64_t vecs, int num_sms) {
   const int64_t slice = std::max<int64_t>(1, (vecs + cluster - 1) / cluster);
   p.cluster = (int)cluster;
   p.slice = (int)slice;
-  p.warps = (int)std::min<int64_t>(kMaxWarps, std::max<int64_t>(2, (slice + 63) / 64));
-  const int64_t most = (int64_t)p.warps * 32 * kPerThread;
-  p.chunks = (int)((slice + most - 1) / most);
+  // Chunks of at most four vectors a thread. All but the last of them exist in
+  // every chunk of every slice: those differ by fewer than 26 vectors.
+  constexpr int64_t kMost = (int64_t)kMaxThreads * kPerThread;
+  p.chunks = (int)((slice + kMost - 1) / kMost);
   p.chunk = (int)((slice + p.chunks - 1) / p.chunks);
+  p.per_thread = p.chunk > kMaxThreads ? kPerThread : 1;
+  p.warps = (int)std::max<int64_t>(2, (p.chunk + 32 * p.per_thread - 1) / (32 * p.per_thread));
   int64_t slots = std::min<int64_t>(kMaxSlots, kRingBytes / ((int64_t)p.chunk * 16));
   if (slots > p.chunks + 3) slots = p.chunks + 3;
   p.slots = (int)slots;
@@ -570,7 +556,7 @@ LossPlan plan_loss(int64_t rows, int64_t vecs, int num_sms) {
 
 // How many clusters of a plan run at once on the current device, kept by the
 // plan since asking takes longer than a launch.
-template <typename T, bool SAME>
+template <typename T, int PT, bool SAME>
 cudaError_t active_clusters(const LossPlan& p, cudaLaunchConfig_t cfg, int num_sms, int* out) {
   struct Known {
     int device, cluster, warps;
@@ -590,7 +576,7 @@ cudaError_t active_clusters(const LossPlan& p, cudaLaunchConfig_t cfg, int num_s
       *out = known[i].clusters;
       return cudaSuccess;
     }
-  auto kernel = loss_rows_kernel<T, SAME>;
+  auto kernel = loss_rows_kernel<T, PT, SAME>;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
@@ -608,7 +594,7 @@ cudaError_t active_clusters(const LossPlan& p, cudaLaunchConfig_t cfg, int num_s
   return cudaSuccess;
 }
 
-template <typename T, bool SAME>
+template <typename T, int PT, bool SAME>
 cudaError_t launch_rows(const LossArgs& a, const LossPlan& p, int num_sms, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
   cfg.blockDim = dim3((unsigned)(p.warps * 32 + 32));
@@ -623,10 +609,10 @@ cudaError_t launch_rows(const LossArgs& a, const LossPlan& p, int num_sms, cudaS
   // As many clusters as run at once: a persistent grid larger than that would
   // leave its last clusters, and their rows, to a second wave.
   int clusters = 0;
-  cudaError_t e = active_clusters<T, SAME>(p, cfg, num_sms, &clusters);
+  cudaError_t e = active_clusters<T, PT, SAME>(p, cfg, num_sms, &clusters);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)(p.whole ? kWholeCtas : std::min<int64_t>(clusters, a.rows) * p.cluster));
-  e = cudaLaunchKernelEx(&cfg, loss_rows_kernel<T, SAME>, a, p);
+  e = cudaLaunchKernelEx(&cfg, loss_rows_kernel<T, PT, SAME>, a, p);
   note_launch();
   return e;
 }
@@ -642,7 +628,10 @@ cudaError_t launch_typed(const LossArgs& a, int num_sms, cudaStream_t s, bool* s
     return cudaGetLastError();
   }
   const bool same = !a.grad || (reinterpret_cast<uintptr_t>(a.logits) - reinterpret_cast<uintptr_t>(a.grad)) % 16 == 0;
-  return same ? launch_rows<T, true>(a, p, num_sms, s) : launch_rows<T, false>(a, p, num_sms, s);
+  if (p.per_thread == 1)
+    return same ? launch_rows<T, 1, true>(a, p, num_sms, s) : launch_rows<T, 1, false>(a, p, num_sms, s);
+  return same ? launch_rows<T, kPerThread, true>(a, p, num_sms, s)
+              : launch_rows<T, kPerThread, false>(a, p, num_sms, s);
 }
 
 }  // namespace
