@@ -29,13 +29,14 @@ namespace dspark {
 
 namespace {
 
-constexpr int kMaxThreads = 512;  // that compute; one warp more issues the copies
+constexpr int kMaxThreads = 256;  // that compute; one warp more issues the copies
 constexpr int kMaxWarps = kMaxThreads / 32;
+constexpr int kSumThreads = 512;  // of the kernels of one CTA per row or per call
 constexpr int kMaxCluster = 16;
 constexpr int kWholeCtas = 8;   // of a launch that is one cluster
 constexpr int kMaxSlots = 8;
-constexpr int kRing = 222 * 1024;  // bytes, at most; the barriers and pairs take 4.4 KB more
-constexpr int kPerThread = 4;  // vectors of a chunk for each thread: 4, or 1 in small chunks
+constexpr int kRing = 108 * 1024;  // bytes, at most: two CTAs per SM, one passing while the other meets
+constexpr int kPerThread = 4;  // vectors of a chunk for each thread: 4, in small chunks 2 or 1
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
 
@@ -173,8 +174,8 @@ __device__ void sum_loss(const LossArgs& a, double* sums) {
   s = block_sum(s, sums);
   if (threadIdx.x == 0) *a.loss = (float)(s * inv_n);
 }
-__global__ void __launch_bounds__(kMaxThreads) loss_sum_kernel(LossArgs a) {
-  __shared__ double sums[kMaxWarps + 1];
+__global__ void __launch_bounds__(kSumThreads) loss_sum_kernel(LossArgs a) {
+  __shared__ double sums[kSumThreads / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   sum_loss(a, sums);
 }
@@ -210,7 +211,7 @@ __device__ __forceinline__ int slice_vectors(const LossPlan& p, int vecs, int ra
 // is copied out as it was copied in; otherwise gradients are written one by one.
 // PT: vectors of a chunk per thread; all but the last exist in every chunk.
 template <typename T, int PT, bool SAME>
-__global__ void __launch_bounds__(kMaxThreads + 32, 1) loss_rows_kernel(LossArgs a, LossPlan p) {
+__global__ void __launch_bounds__(kMaxThreads + 32, 2) loss_rows_kernel(LossArgs a, LossPlan p) {
   constexpr int kE = Vectors<T>::kE;
   extern __shared__ __align__(128) uint4 ring[];
   __shared__ RowBarriers bars;
@@ -398,19 +399,32 @@ __global__ void __launch_bounds__(kMaxThreads + 32, 1) loss_rows_kernel(LossArgs
         __syncwarp();
         const float row_xt = xt, row_edge = edge;
         if (next_live) load_singles(next, next_t);
+        // The target's place in this slice, as chunk and vector, if any.
+        const int at = (int)t - shape.head, vec = at >= 0 ? at / kE - rank * p.slice : -1, te = at % kE;
+        const int tc = vec >= 0 && vec < count ? vec / p.chunk : -1, tj = vec - tc * p.chunk;
+        const bool own_target = tc >= 0 && tj % threads == tid;
+        const float scale = (float)((double)w * inv_n);
         mbar_wait_cluster(&bars.met[parity], met_phase, ctl);
-        m = -INFINITY;
-        for (int k = lane; k < ranks * warps; k += 32) m = fmaxf(m, pairs[parity][k].x);
+        // Each warp for itself, a lane for up to four pairs.
+        float2 met[kMaxCluster * kMaxWarps / 32];
+        uint32_t high = 0u;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int k = 0; k < kMaxCluster * kMaxWarps / 32; ++k) {
+          met[k] = lane + 32 * k < ranks * warps ? pairs[parity][lane + 32 * k] : make_float2(-INFINITY, 0.0f);
+          // Without NaN (orderable above all): a warp's maximum is NaN only where it has no number at all.
+          high = max(high, met[k].x == met[k].x ? orderable_bits(met[k].x) : 0u);
+        }
+        high = __reduce_max_sync(0xffffffffu, high);
+        m = __uint_as_float((high & 0x80000000u) ? high & 0x7fffffffu : ~high);
         s = 0.0f;
-        for (int k = lane; k < ranks * warps; k += 32) s += rescaled(pairs[parity][k].y, pairs[parity][k].x, m);
+#pragma unroll
+        for (int k = 0; k < kMaxCluster * kMaxWarps / 32; ++k) s += rescaled(met[k].y, met[k].x, m);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         parity ^= 1;
         if (parity == 0) met_phase ^= 1u;
         if (isinf(m)) s = NAN;  // +inf somewhere, or -inf everywhere
-        const float scale = (float)((double)w * inv_n), factor = scale / s, unit = unit_for(m), ref = reference(m);
+        const float factor = scale / s, unit = unit_for(m), ref = reference(m);
         if (rank == 0 && tid == 0)  // in plain units where the exponents' would overflow
           a.row_losses[i] = unit == kLog2e && fabsf(row_xt) <= 0x1p126f
                                 ? kLn2 * (log2f(s) - fmaf(row_xt, unit, -ref))
@@ -421,10 +435,7 @@ __global__ void __launch_bounds__(kMaxThreads + 32, 1) loss_rows_kernel(LossArgs
           const int v = shape.edge(tid);
           g[v] = from_f32<T>(v == (int)t ? at_target : ex2(fmaf(row_edge, unit, -ref)) * factor);
         }
-        // Pass 2. The target's place in this slice, as chunk and vector, if any.
-        const int at = (int)t - shape.head, vec = at >= 0 ? at / kE - rank * p.slice : -1, te = at % kE;
-        const int tc = vec >= 0 && vec < count ? vec / p.chunk : -1, tj = vec - tc * p.chunk;
-        const bool own_target = tc >= 0 && tj % threads == tid;
+        // Pass 2.
         T* to = g + shape.head + (int64_t)rank * p.slice * kE;
         for (int c = 0; c < p.chunks; ++c) {
           const int n = chunk_vectors(p, count, c);
@@ -474,9 +485,9 @@ __global__ void __launch_bounds__(kMaxThreads + 32, 1) loss_rows_kernel(LossArgs
 
 // Rows longer than a cluster's shared memory: one CTA per row reads it twice.
 template <typename T>
-__global__ void __launch_bounds__(kMaxThreads) loss_long_rows_kernel(LossArgs a) {
-  __shared__ double sums[kMaxWarps + 1];
-  __shared__ float2 parts[kMaxWarps];
+__global__ void __launch_bounds__(kSumThreads) loss_long_rows_kernel(LossArgs a) {
+  __shared__ double sums[kSumThreads / 32];
+  __shared__ float2 parts[kSumThreads / 32];
   const double inv_n = inverse_total(a, sums, false);
   for (int64_t i = blockIdx.x; i < a.rows; i += gridDim.x) {
     int64_t t;
@@ -527,7 +538,7 @@ __global__ void __launch_bounds__(kMaxThreads) loss_long_rows_kernel(LossArgs a)
 // The cluster and ring for a row of `vecs` vectors, or cluster 0 where none
 // holds it.
 LossPlan plan_loss(int64_t rows, int64_t vecs, int num_sms) {
-  constexpr int64_t kMaxSlice = 9728;  // vectors; 152 KB, so that the ring has room beyond a slice
+  constexpr int64_t kMaxSlice = 4864;  // vectors; 76 KB, so that the ring has room beyond a slice
   constexpr int64_t kRingBytes = kRing;
   int64_t cluster = 1;
   while (cluster <= kMaxCluster && cluster * kMaxSlice < vecs) cluster *= 2;
@@ -546,7 +557,7 @@ LossPlan plan_loss(int64_t rows, int64_t vecs, int num_sms) {
   constexpr int64_t kMost = (int64_t)kMaxThreads * kPerThread;
   p.chunks = (int)((slice + kMost - 1) / kMost);
   p.chunk = (int)((slice + p.chunks - 1) / p.chunks);
-  p.per_thread = p.chunk > kMaxThreads ? kPerThread : 1;
+  p.per_thread = p.chunk > 2 * kMaxThreads ? kPerThread : p.chunk > kMaxThreads ? 2 : 1;
   p.warps = (int)std::max<int64_t>(2, (p.chunk + 32 * p.per_thread - 1) / (32 * p.per_thread));
   int64_t slots = std::min<int64_t>(kMaxSlots, kRingBytes / ((int64_t)p.chunk * 16));
   if (slots > p.chunks + 3) slots = p.chunks + 3;
@@ -623,11 +634,13 @@ cudaError_t launch_typed(const LossArgs& a, int num_sms, cudaStream_t s, bool* s
   *summed = p.whole != 0;
   if (p.cluster == 0) {
     const int64_t grid = a.rows < 2ll * num_sms ? a.rows : 2ll * num_sms;
-    loss_long_rows_kernel<T><<<(unsigned)grid, kMaxThreads, 0, s>>>(a);
+    loss_long_rows_kernel<T><<<(unsigned)grid, kSumThreads, 0, s>>>(a);
     note_launch();
     return cudaGetLastError();
   }
   const bool same = !a.grad || (reinterpret_cast<uintptr_t>(a.logits) - reinterpret_cast<uintptr_t>(a.grad)) % 16 == 0;
+  if (p.per_thread == 2)
+    return same ? launch_rows<T, 2, true>(a, p, num_sms, s) : launch_rows<T, 2, false>(a, p, num_sms, s);
   if (p.per_thread == 1)
     return same ? launch_rows<T, 1, true>(a, p, num_sms, s) : launch_rows<T, 1, false>(a, p, num_sms, s);
   return same ? launch_rows<T, kPerThread, true>(a, p, num_sms, s)
@@ -645,7 +658,7 @@ cudaError_t launch_loss(const LossArgs& a, int logits_dtype, int num_sms, cudaSt
   }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(kMaxThreads);
+  cfg.blockDim = dim3(kSumThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr{};  // its launch overlaps the rows; it waits for their end
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
