@@ -5,18 +5,19 @@
 // (sum), d loss / d c_v = w_i / N (exp(c_v - lse) - [v = t]).
 //
 // The sum and the gradient both need the whole row, so a kernel that streams
-// reads it twice. Here a cluster of CTAs keeps a row in its shared memory (a
-// 129280-id bf16 row is 252 KB, more than one SM's): each logit is read once
-// and each gradient written once, 4 bytes per bf16 logit, and that traffic is
-// the bound.
+// reads it twice. Here a cluster of CTAs keeps a row in its registers (a
+// 129280-id bf16 row is 252 KB, a quarter of it in each of four CTAs): each
+// logit is read once and each gradient written once, 4 bytes per bf16 logit,
+// and that traffic is the bound.
 //
-// A CTA's slice of a row lies in a ring of chunks, filled and emptied by bulk
-// copies that one thread issues. Pass 1 walks the chunks as they land, every
-// thread with its own running maximum m and sum s of 2^(c log2 e - r), where
+// Pass 1: every thread takes its maximum m and sum s of 2^(c log2 e - r), where
 // the reference r = m log2 e is rounded; the warps' pairs (m, s) meet in every
-// CTA of the cluster. Pass 2 overwrites the chunks by the gradient, each copied
-// out as it is done and its place filled with the next row's chunk. All of a
-// row goes by rounded references, so their rounding cancels.
+// CTA of the cluster. Pass 2 turns the registers into the gradient, and each
+// vector's registers load the next row's as soon as it is written. All of a
+// row goes by rounded references, so their rounding cancels. Two CTAs share an
+// SM, so that one passes while the other meets. Plain loads and stores carry
+// more here than bulk copies through shared memory, which held the same kernel
+// to 4.3 TB/s whatever it computed.
 #include <algorithm>
 #include <cmath>
 #include <mutex>
@@ -29,14 +30,12 @@ namespace dspark {
 
 namespace {
 
-constexpr int kMaxThreads = 256;  // that compute; one warp more issues the copies
+constexpr int kMaxThreads = 256;
 constexpr int kMaxWarps = kMaxThreads / 32;
 constexpr int kSumThreads = 512;  // of the kernels of one CTA per row or per call
 constexpr int kMaxCluster = 16;
-constexpr int kWholeCtas = 8;   // of a launch that is one cluster
-constexpr int kMaxSlots = 8;
-constexpr int kRing = 108 * 1024;  // bytes, at most: two CTAs per SM, one passing while the other meets
-constexpr int kPerThread = 4;  // vectors of a chunk for each thread: 4, in small chunks 2 or 1
+constexpr int kWholeCtas = 8;     // of a launch that is one cluster
+constexpr int kMaxVectors = 16;   // of a row, in a thread's registers
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
 
@@ -182,300 +181,212 @@ __global__ void __launch_bounds__(kSumThreads) loss_sum_kernel(LossArgs a) {
 
 struct LossPlan {
   int cluster;  // CTAs per row
-  int warps;    // that compute, per CTA
+  int threads;  // per CTA
   int slice;    // vectors of a row per CTA
-  int chunk;    // vectors per chunk, at most 32 per_thread warps
-  int per_thread;
-  int chunks;   // chunks per slice
-  int slots;    // chunks in the ring, at least `chunks`
+  int vectors;  // of them per thread, at most
   int whole;    // the launch is one hardware cluster, a CTA per row, which also sums the loss
 };
 
-struct RowBarriers {
-  uint64_t full[kMaxSlots];  // a chunk has landed
-  uint64_t done[kMaxSlots];  // every warp has left a chunk
-  uint64_t met[2];           // a row's pairs are here
-};
-
-// Chunk c of a slice of `count` vectors: the vectors in it.
-__device__ __forceinline__ int chunk_vectors(const LossPlan& p, int count, int c) {
-  return max(0, min(p.chunk, count - c * p.chunk));
-}
 // The vectors of a row that lie in CTA `rank`'s slice.
 __device__ __forceinline__ int slice_vectors(const LossPlan& p, int vecs, int rank) {
   return max(0, min(p.slice, vecs - rank * p.slice));
 }
 
 // SAME: the gradient's rows start at the same offset from a 16-byte address as
-// the logits' (in place, or any vocabulary of whole vectors), so that a chunk
-// is copied out as it was copied in; otherwise gradients are written one by one.
-// PT: vectors of a chunk per thread; all but the last exist in every chunk.
-template <typename T, int PT, bool SAME>
-__global__ void __launch_bounds__(kMaxThreads + 32, 2) loss_rows_kernel(LossArgs a, LossPlan p) {
+// the logits' (in place, or any vocabulary of whole vectors), so that a vector
+// read is a vector written; otherwise gradients are written one by one.
+template <typename T, int NV, bool SAME>
+__global__ void __launch_bounds__(kMaxThreads, 2) loss_rows_kernel(LossArgs a, LossPlan p) {
   constexpr int kE = Vectors<T>::kE;
-  extern __shared__ __align__(128) uint4 ring[];
-  __shared__ RowBarriers bars;
+  __shared__ uint64_t met_bar[2];  // a row's pairs are here
   __shared__ float2 pairs[2][kMaxCluster * kMaxWarps];
-  __shared__ double sums[kMaxWarps + 1];
+  __shared__ double sums[kMaxWarps];
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = (int)threadIdx.x;
-  const int ranks = p.cluster, rank = ranks > 1 ? (int)cluster_rank() : 0, warps = p.warps, threads = warps * 32;
-  const int64_t step = gridDim.x / ranks, first = blockIdx.x / ranks;
-  const int vocab = (int)a.vocab;
+  const int threads = (int)blockDim.x, warps = threads >> 5;
+  const int ranks = p.cluster, rank = ranks > 1 ? (int)cluster_rank() : 0;
+  const int step = (int)gridDim.x / ranks, rows = (int)a.rows, vocab = (int)a.vocab;
   const T* logits = static_cast<const T*>(a.logits);
   T* grads = static_cast<T*>(a.grad);
   const WaitCtl ctl{&abort_flag, a.status, a.wait_limit_ns};
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // The next live row at or after i.
-  auto seek = [&](int64_t i, int64_t* t, float* w) {
-    while (i < a.rows && !live_row(a, i, t, w)) i += step;
-    return i;
-  };
-
   if (tid == 0) {
     abort_flag = 0;
-    for (int k = 0; k < p.slots; ++k) {
-      mbar_init(&bars.full[k], 1);
-      mbar_init(&bars.done[k], (uint32_t)warps);
-    }
-    mbar_init(&bars.met[0], (uint32_t)(ranks * warps));
-    mbar_init(&bars.met[1], (uint32_t)(ranks * warps));
+    mbar_init(&met_bar[0], (uint32_t)(ranks * warps));
+    mbar_init(&met_bar[1], (uint32_t)(ranks * warps));
     fence_barrier_init();
+  }
+
+  int i = (int)blockIdx.x / ranks, t = 0;  // the row and its target
+  float w = 0.0f;
+  auto look_up = [&](int row, int* target, float* weight) {
+    int64_t id = 0;
+    const bool live = row < rows && live_row(a, row, &id, weight);
+    *target = (int)id;
+    return live;
+  };
+  uint4 raw[NV];                       // this thread's vectors: tid + n threads of the slice
+  float edge = -INFINITY, xt = 0.0f;   // its edge element; the target's logit
+  auto load_singles = [&](int row, int target) {
+    const T* c = logits + (int64_t)row * vocab;
+    const RowShape<T> shape(c, vocab);
+    edge = rank == 0 && tid < shape.edges ? to_f32(c[shape.edge(tid)]) : -INFINITY;
+    xt = to_f32(c[target]);
+  };
+  // Where a vector is not in the slice its registers hold -inf; only rows that
+  // do not all begin alike change which those are.
+  const bool ragged = vocab % kE != 0;
+  auto load = [&](const uint4* from, int left, int n) {
+    if (n * threads < left)
+      raw[n] = __ldcs(from + n * threads);
+    else if (ragged)
+      raw[n] = make_uint4(Vectors<T>::kFill, Vectors<T>::kFill, Vectors<T>::kFill, Vectors<T>::kFill);
+  };
+#pragma unroll
+  for (int n = 0; n < NV; ++n)
+    raw[n] = make_uint4(Vectors<T>::kFill, Vectors<T>::kFill, Vectors<T>::kFill, Vectors<T>::kFill);
+  bool live = look_up(i, &t, &w);
+  if (live) {
+    const T* c = logits + (int64_t)i * vocab;
+    const RowShape<T> shape(c, vocab);
+    const uint4* from = reinterpret_cast<const uint4*>(c + shape.head) + (int64_t)rank * p.slice + tid;
+    const int left = slice_vectors(p, shape.vecs, rank) - tid;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) load(from, left, n);
+    load_singles(i, t);
   }
   const double inv_n = inverse_total(a, sums, false);
   __syncthreads();
   if (ranks > 1) cluster_barrier();  // every CTA's barriers are there
 
-  if (warp == warps) {
-    if (lane == 0) {
-      // The copies: chunk q goes to slot q % slots once the chunk that was
-      // there has been copied out.
-      int64_t t;
-      float w;
-      int64_t out_row = first, in_row = first;
-      int out_c = 0, slot = 0, out_slot = 0;
-      uint32_t out_phase = 0;
-      int64_t in_flight = 0;  // chunks loaded and not yet copied out
-      out_row = seek(out_row, &t, &w);
-      auto copy_out = [&]() {
-        if (!mbar_wait(&bars.done[out_slot], out_phase, ctl)) return false;
-        if (SAME && grads) {
-          const RowShape<T> shape(logits + out_row * vocab, vocab);
-          const int n = chunk_vectors(p, slice_vectors(p, shape.vecs, rank), out_c);
-          if (n > 0) {
-            T* to = grads + out_row * vocab + shape.head + ((int64_t)rank * p.slice + out_c * p.chunk) * kE;
-            bulk_store(to, ring + (size_t)out_slot * p.chunk, (uint32_t)n * 16u);
-            bulk_commit_group();
-            bulk_wait_group_read<0>();
-          }
-        }
-        if (++out_slot == p.slots) {
-          out_slot = 0;
-          out_phase ^= 1u;
-        }
-        if (++out_c == p.chunks) {
-          out_c = 0;
-          out_row = seek(out_row + step, &t, &w);
-        }
-        --in_flight;
-        return true;
-      };
-      bool ok = true;
-      for (in_row = seek(in_row, &t, &w); ok && in_row < a.rows; in_row = seek(in_row + step, &t, &w)) {
-        const RowShape<T> shape(logits + in_row * vocab, vocab);
-        const int count = slice_vectors(p, shape.vecs, rank);
-        const T* from = logits + in_row * vocab + shape.head + (int64_t)rank * p.slice * kE;
-        for (int c = 0; c < p.chunks; ++c) {
-          if (in_flight == p.slots && !(ok = copy_out())) break;
-          const int n = chunk_vectors(p, count, c);
-          if (n > 0) {
-            mbar_arrive_expect_tx(&bars.full[slot], (uint32_t)n * 16u);
-            bulk_load(ring + (size_t)slot * p.chunk, from + (int64_t)c * p.chunk * kE, (uint32_t)n * 16u,
-                      &bars.full[slot]);
-          } else {
-            mbar_arrive(&bars.full[slot]);
-          }
-          ++in_flight;
-          if (++slot == p.slots) slot = 0;
-        }
-      }
-      while (ok && in_flight > 0) ok = copy_out();
-      bulk_wait_group<0>();
-      // After a wait that ran out, copies still under way end before the CTA does.
-      if (!ok) {
-        const uint64_t t0 = globaltimer_ns();
-        for (int k = 0; k < p.slots && in_flight > 0; ++k)
-          for (uint32_t phase = 0; phase < 2; ++phase)
-            while (!mbar_try_wait(&bars.full[k], phase) && globaltimer_ns() - t0 < a.wait_limit_ns) {
-            }
-      }
-    }
-    __syncwarp();
-  } else {
-    int slot1 = 0, slot2 = 0, parity = 0;  // of pass 1 and pass 2 in the ring; of the pairs' buffer
-    uint32_t phase1 = 0, met_phase = 0;
-    int64_t i = first;
-    int64_t t = 0;
-    float w = 0.0f;
-    float edge = -INFINITY, xt = 0.0f;  // this thread's edge element; the target's logit
-    auto load_singles = [&](int64_t row, int64_t target) {
-      const T* c = logits + row * vocab;
-      const RowShape<T> shape(c, vocab);
-      edge = rank == 0 && tid < shape.edges ? to_f32(c[shape.edge(tid)]) : -INFINITY;
-      xt = to_f32(c[target]);
-    };
-    bool live = i < a.rows && live_row(a, i, &t, &w);
-    if (live) load_singles(i, t);
-    while (i < a.rows) {
-      const int64_t next = i + step;
-      int64_t next_t = 0;
-      float next_w = 0.0f;
-      const bool next_live = next < a.rows && live_row(a, next, &next_t, &next_w);
-      const RowShape<T> shape(logits + i * vocab, vocab);
-      const int count = slice_vectors(p, shape.vecs, rank);
-      T* g = grads ? grads + i * vocab : nullptr;
-      if (!live) {
-        if (rank == 0 && tid == 0) a.row_losses[i] = 0.0f;
-        if (g) {
-          if (rank == 0 && tid < shape.edges) g[shape.edge(tid)] = from_f32<T>(0.0f);
-          T* to = g + shape.head + (int64_t)rank * p.slice * kE;
+  int parity = 0;
+  uint32_t met_phase = 0;
+  while (i < rows) {
+    const int next = rows - i > step ? i + step : rows;
+    int next_t = 0;
+    float next_w = 0.0f;
+    const bool next_live = look_up(next, &next_t, &next_w);
+    const RowShape<T> shape(logits + (int64_t)i * vocab, vocab);
+    const int count = slice_vectors(p, shape.vecs, rank);
+    const int left = grads ? count - tid : 0;
+    T* g = grads ? grads + (int64_t)i * vocab : nullptr;
+    T* to = g + shape.head + ((int64_t)rank * p.slice + tid) * kE;
+    const T* cn = logits + (int64_t)next * vocab;
+    const RowShape<T> next_shape(cn, vocab);
+    const uint4* from = reinterpret_cast<const uint4*>(cn + next_shape.head) + (int64_t)rank * p.slice + tid;
+    const int next_left = next_live ? slice_vectors(p, next_shape.vecs, rank) - tid : 0;
+    if (!live) {
+      if (rank == 0 && tid == 0) a.row_losses[i] = 0.0f;
+      if (g && rank == 0 && tid < shape.edges) g[shape.edge(tid)] = from_f32<T>(0.0f);
+#pragma unroll
+      for (int n = 0; n < NV; ++n) {
+        if (n * threads < left) {
           if (SAME) {
-            for (int j = tid; j < count; j += threads)
-              __stcs(reinterpret_cast<uint4*>(to) + j, make_uint4(0u, 0u, 0u, 0u));
+            __stcs(reinterpret_cast<uint4*>(to) + n * threads, make_uint4(0u, 0u, 0u, 0u));
           } else {
-            for (int j = tid; j < count * kE; j += threads) to[j] = from_f32<T>(0.0f);
+#pragma unroll
+            for (int e = 0; e < kE; ++e) to[n * threads * kE + e] = from_f32<T>(0.0f);
           }
         }
-        if (next_live) load_singles(next, next_t);
-      } else {
-        // Pass 1. A thread of -inf alone keeps m = -inf and sums zeros (or NaN).
-        float m = edge;
-        float s = edge == -INFINITY ? 0.0f : ex2(fmaf(edge, unit_for(edge), -reference(edge)));
-        for (int c = 0; c < p.chunks; ++c) {
-          mbar_wait(&bars.full[slot1], phase1, ctl);
-          const int n = chunk_vectors(p, count, c);
-          const uint4* from = ring + (size_t)slot1 * p.chunk + tid;
-          uint4 raw[PT];
-#pragma unroll
-          for (int k = 0; k < PT - 1; ++k) raw[k] = from[k * threads];
-          raw[PT - 1] = make_uint4(Vectors<T>::kFill, Vectors<T>::kFill, Vectors<T>::kFill, Vectors<T>::kFill);
-          if (tid + (PT - 1) * threads < n) raw[PT - 1] = from[(PT - 1) * threads];
-          float top = m;
-#pragma unroll
-          for (int k = 0; k < PT; ++k) top = fmaxf(top, Vectors<T>::max_of(raw[k]));
-          s = rescaled(s, m, top);
-          m = top;
-          const float unit = unit_for(top), ref = reference(top);
-          float part[2] = {0.0f, 0.0f};
-#pragma unroll
-          for (int k = 0; k < PT; ++k)
-#pragma unroll
-            for (int e = 0; e < kE; ++e) part[e & 1] += ex2(fmaf(Vectors<T>::get(raw[k], e), unit, -ref));
-          s += part[0] + part[1];
-          if (++slot1 == p.slots) {
-            slot1 = 0;
-            phase1 ^= 1u;
-          }
-        }
-        float top = m;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        s = rescaled(s, m, top);
-        m = top;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        // The warp's pair to every CTA. The other of the two buffers may still
-        // be read; this one was left by all warps before they sent the pairs
-        // that ended the last row's wait.
-        if (ranks > 1) {
-          if (lane < ranks) {
-            store_remote(remote_u32(&pairs[parity][rank * warps + warp], (uint32_t)lane), m, s);
-            mbar_arrive_remote(remote_u32(&bars.met[parity], (uint32_t)lane));
-          }
-        } else if (lane == 0) {
-          pairs[parity][warp] = make_float2(m, s);
-          mbar_arrive(&bars.met[parity]);
-        }
-        __syncwarp();
-        const float row_xt = xt, row_edge = edge;
-        if (next_live) load_singles(next, next_t);
-        // The target's place in this slice, as chunk and vector, if any.
-        const int at = (int)t - shape.head, vec = at >= 0 ? at / kE - rank * p.slice : -1, te = at % kE;
-        const int tc = vec >= 0 && vec < count ? vec / p.chunk : -1, tj = vec - tc * p.chunk;
-        const bool own_target = tc >= 0 && tj % threads == tid;
-        const float scale = (float)((double)w * inv_n);
-        mbar_wait_cluster(&bars.met[parity], met_phase, ctl);
-        // Each warp for itself, a lane for up to four pairs.
-        float2 met[kMaxCluster * kMaxWarps / 32];
-        uint32_t high = 0u;
-#pragma unroll
-        for (int k = 0; k < kMaxCluster * kMaxWarps / 32; ++k) {
-          met[k] = lane + 32 * k < ranks * warps ? pairs[parity][lane + 32 * k] : make_float2(-INFINITY, 0.0f);
-          // Without NaN (orderable above all): a warp's maximum is NaN only where it has no number at all.
-          high = max(high, met[k].x == met[k].x ? orderable_bits(met[k].x) : 0u);
-        }
-        high = __reduce_max_sync(0xffffffffu, high);
-        m = __uint_as_float((high & 0x80000000u) ? high & 0x7fffffffu : ~high);
-        s = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kMaxCluster * kMaxWarps / 32; ++k) s += rescaled(met[k].y, met[k].x, m);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        parity ^= 1;
-        if (parity == 0) met_phase ^= 1u;
-        if (isinf(m)) s = NAN;  // +inf somewhere, or -inf everywhere
-        const float factor = scale / s, unit = unit_for(m), ref = reference(m);
-        if (rank == 0 && tid == 0)  // in plain units where the exponents' would overflow
-          a.row_losses[i] = unit == kLog2e && fabsf(row_xt) <= 0x1p126f
-                                ? kLn2 * (log2f(s) - fmaf(row_xt, unit, -ref))
-                                : logf(s) + (m - row_xt);
-        // The gradient at the target, which its owner writes over the rest.
-        const float at_target = ex2(fmaf(row_xt, unit, -ref)) * factor - scale;
-        if (g && rank == 0 && tid < shape.edges) {
-          const int v = shape.edge(tid);
-          g[v] = from_f32<T>(v == (int)t ? at_target : ex2(fmaf(row_edge, unit, -ref)) * factor);
-        }
-        // Pass 2.
-        T* to = g + shape.head + (int64_t)rank * p.slice * kE;
-        for (int c = 0; c < p.chunks; ++c) {
-          const int n = chunk_vectors(p, count, c);
-          uint4* place = ring + (size_t)slot2 * p.chunk + tid;
-          if (g) {
-#pragma unroll
-            for (int k = 0; k < PT; ++k) {
-              const int j = tid + k * threads;
-              if (k == PT - 1 && j >= n) break;
-              const uint4 raw = place[k * threads];
-              float x[kE];
-#pragma unroll
-              for (int e = 0; e < kE; ++e) x[e] = ex2(fmaf(Vectors<T>::get(raw, e), unit, -ref)) * factor;
-              if (SAME) {
-                place[k * threads] = Vectors<T>::pack(x);
-              } else {
-#pragma unroll
-                for (int e = 0; e < kE; ++e) to[((int64_t)c * p.chunk + j) * kE + e] = from_f32<T>(x[e]);
-              }
-            }
-            if (own_target && c == tc) {
-              if (SAME)
-                reinterpret_cast<T*>(ring + (size_t)slot2 * p.chunk + tj)[te] = from_f32<T>(at_target);
-              else
-                g[t] = from_f32<T>(at_target);
-            }
-          }
-          if (SAME) fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.done[slot2]);
-          if (++slot2 == p.slots) slot2 = 0;
-        }
+        load(from, next_left, n);
       }
-      i = next;
-      t = next_t;
-      w = next_w;
-      live = next_live;
+      if (next_live) load_singles(next, next_t);
+    } else {
+      // Pass 1. A thread of -inf alone keeps m = -inf and sums zeros (or NaN).
+      float m = edge;
+#pragma unroll
+      for (int n = 0; n < NV; ++n) m = fmaxf(m, Vectors<T>::max_of(raw[n]));
+      float s;
+      {
+        const float unit = unit_for(m), ref = reference(m);
+        float part[4] = {ex2(fmaf(edge, unit, -ref)), 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+          for (int e = 0; e < kE; ++e) part[e & 3] += ex2(fmaf(Vectors<T>::get(raw[n], e), unit, -ref));
+        s = (part[0] + part[1]) + (part[2] + part[3]);
+      }
+      float top = m;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      s = rescaled(s, m, top);
+      m = top;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      // The warp's pair to every CTA. The other of the two buffers may still
+      // be read; this one was left by all warps before they sent the pairs
+      // that ended the last row's wait.
+      if (ranks > 1) {
+        if (lane < ranks) {
+          store_remote(remote_u32(&pairs[parity][rank * warps + warp], (uint32_t)lane), m, s);
+          mbar_arrive_remote(remote_u32(&met_bar[parity], (uint32_t)lane));
+        }
+      } else if (lane == 0) {
+        pairs[parity][warp] = make_float2(m, s);
+        mbar_arrive(&met_bar[parity]);
+      }
+      __syncwarp();
+      const float row_xt = xt, row_edge = edge;
+      if (next_live) load_singles(next, next_t);
+      // Whether the target is in one of this thread's vectors.
+      const int at = t - shape.head, vec = at >= 0 ? at / kE - rank * p.slice : -1;
+      const bool own_target = vec >= 0 && vec < count && vec % threads == tid;
+      const float scale = (float)((double)w * inv_n);
+      mbar_wait_cluster(&met_bar[parity], met_phase, ctl);
+      // Each warp for itself, a lane for up to four pairs.
+      float2 met[kMaxCluster * kMaxWarps / 32];
+      uint32_t high = 0u;
+#pragma unroll
+      for (int k = 0; k < kMaxCluster * kMaxWarps / 32; ++k) {
+        met[k] = lane + 32 * k < ranks * warps ? pairs[parity][lane + 32 * k] : make_float2(-INFINITY, 0.0f);
+        // Without NaN (orderable above all): a warp's maximum is NaN only where it has no number at all.
+        high = max(high, met[k].x == met[k].x ? orderable_bits(met[k].x) : 0u);
+      }
+      high = __reduce_max_sync(0xffffffffu, high);
+      m = __uint_as_float((high & 0x80000000u) ? high & 0x7fffffffu : ~high);
+      s = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kMaxCluster * kMaxWarps / 32; ++k) s += rescaled(met[k].y, met[k].x, m);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      parity ^= 1;
+      if (parity == 0) met_phase ^= 1u;
+      if (isinf(m)) s = NAN;  // +inf somewhere, or -inf everywhere
+      const float factor = scale / s, unit = unit_for(m), ref = reference(m);
+      if (rank == 0 && tid == 0)  // in plain units where the exponents' would overflow
+        a.row_losses[i] = unit == kLog2e && fabsf(row_xt) <= 0x1p126f
+                              ? kLn2 * (log2f(s) - fmaf(row_xt, unit, -ref))
+                              : logf(s) + (m - row_xt);
+      // The gradient at the target, which its owner writes over the rest.
+      const float at_target = ex2(fmaf(row_xt, unit, -ref)) * factor - scale;
+      if (g && rank == 0 && tid < shape.edges) {
+        const int v = shape.edge(tid);
+        g[v] = from_f32<T>(v == t ? at_target : ex2(fmaf(row_edge, unit, -ref)) * factor);
+      }
+      // Pass 2.
+#pragma unroll
+      for (int n = 0; n < NV; ++n) {
+        if (n * threads < left) {
+          float x[kE];
+#pragma unroll
+          for (int e = 0; e < kE; ++e) x[e] = ex2(fmaf(Vectors<T>::get(raw[n], e), unit, -ref)) * factor;
+          if (SAME) {
+            __stcs(reinterpret_cast<uint4*>(to) + n * threads, Vectors<T>::pack(x));
+          } else {
+#pragma unroll
+            for (int e = 0; e < kE; ++e) to[n * threads * kE + e] = from_f32<T>(x[e]);
+          }
+        }
+        load(from, next_left, n);
+      }
+      if (g && own_target) g[t] = from_f32<T>(at_target);  // after the vector that holds it, by the same thread
     }
-    __syncwarp();
+    i = next;
+    t = next_t;
+    w = next_w;
+    live = next_live;
   }
+  __syncwarp();
   if (ranks > 1) cluster_barrier();  // no CTA leaves while others may still send to it
   if (p.whole) {
     cluster_barrier();  // every row's loss is written
@@ -483,7 +394,7 @@ __global__ void __launch_bounds__(kMaxThreads + 32, 2) loss_rows_kernel(LossArgs
   }
 }
 
-// Rows longer than a cluster's shared memory: one CTA per row reads it twice.
+// Rows longer than a cluster's registers: one CTA per row reads it twice.
 template <typename T>
 __global__ void __launch_bounds__(kSumThreads) loss_long_rows_kernel(LossArgs a) {
   __shared__ double sums[kSumThreads / 32];
@@ -535,11 +446,9 @@ __global__ void __launch_bounds__(kSumThreads) loss_long_rows_kernel(LossArgs a)
   }
 }
 
-// The cluster and ring for a row of `vecs` vectors, or cluster 0 where none
-// holds it.
+// The cluster for a row of `vecs` vectors, or cluster 0 where none holds it.
 LossPlan plan_loss(int64_t rows, int64_t vecs, int num_sms) {
-  constexpr int64_t kMaxSlice = 4864;  // vectors; 76 KB, so that the ring has room beyond a slice
-  constexpr int64_t kRingBytes = kRing;
+  constexpr int64_t kMaxSlice = (int64_t)kMaxThreads * kMaxVectors;
   int64_t cluster = 1;
   while (cluster <= kMaxCluster && cluster * kMaxSlice < vecs) cluster *= 2;
   LossPlan p{};
@@ -548,68 +457,56 @@ LossPlan plan_loss(int64_t rows, int64_t vecs, int num_sms) {
   // a time, instead of a second kernel for the sum.
   p.whole = cluster == 1 && rows <= 64 && rows * vecs <= 16384 ? 1 : 0;
   // Few rows: more CTAs for each.
-  while (!p.whole && rows * cluster * 2 <= num_sms && cluster < 8 && vecs >= cluster * 2 * 512) cluster *= 2;
+  while (!p.whole && rows * cluster * 2 <= 2 * num_sms && cluster < 8 && vecs >= cluster * 2 * 512) cluster *= 2;
   const int64_t slice = std::max<int64_t>(1, (vecs + cluster - 1) / cluster);
   p.cluster = (int)cluster;
   p.slice = (int)slice;
-  // Chunks of at most four vectors a thread. All but the last of them exist in
-  // every chunk of every slice: those differ by fewer than 26 vectors.
-  constexpr int64_t kMost = (int64_t)kMaxThreads * kPerThread;
-  p.chunks = (int)((slice + kMost - 1) / kMost);
-  p.chunk = (int)((slice + p.chunks - 1) / p.chunks);
-  p.per_thread = p.chunk > 2 * kMaxThreads ? kPerThread : p.chunk > kMaxThreads ? 2 : 1;
-  p.warps = (int)std::max<int64_t>(2, (p.chunk + 32 * p.per_thread - 1) / (32 * p.per_thread));
-  int64_t slots = std::min<int64_t>(kMaxSlots, kRingBytes / ((int64_t)p.chunk * 16));
-  if (slots > p.chunks + 3) slots = p.chunks + 3;
-  p.slots = (int)slots;
+  p.vectors = 1;
+  while ((int64_t)p.vectors * kMaxThreads < slice) p.vectors *= 2;
+  p.threads = (int)std::max<int64_t>(64, (slice + 32 * p.vectors - 1) / (32 * p.vectors) * 32);
   return p;
 }
 
 // How many clusters of a plan run at once on the current device, kept by the
 // plan since asking takes longer than a launch.
-template <typename T, int PT, bool SAME>
+template <typename T, int NV, bool SAME>
 cudaError_t active_clusters(const LossPlan& p, cudaLaunchConfig_t cfg, int num_sms, int* out) {
   struct Known {
-    int device, cluster, warps;
-    size_t bytes;
-    int clusters;
+    int device, cluster, threads, clusters;
   };
   static std::mutex mu;
-  static Known known[16];
+  static Known known[32];
   static int count = 0;
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lock(mu);
-  for (int i = 0; i < std::min(count, 16); ++i)
-    if (known[i].device == device && known[i].cluster == p.cluster && known[i].warps == p.warps &&
-        known[i].bytes == cfg.dynamicSmemBytes) {
+  for (int i = 0; i < std::min(count, 32); ++i)
+    if (known[i].device == device && known[i].cluster == p.cluster && known[i].threads == p.threads) {
       *out = known[i].clusters;
       return cudaSuccess;
     }
-  auto kernel = loss_rows_kernel<T, PT, SAME>;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  auto kernel = loss_rows_kernel<T, NV, SAME>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   int clusters = 0;
   if (p.cluster > 1) {
     cfg.gridDim = dim3((unsigned)p.cluster);
     e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
   } else {
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&clusters, kernel, (int)cfg.blockDim.x, cfg.dynamicSmemBytes);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&clusters, kernel, p.threads, 0);
     clusters *= num_sms;
   }
   if (e != cudaSuccess) return e;
   *out = std::max(clusters, 1);
-  known[count++ % 16] = Known{device, p.cluster, p.warps, cfg.dynamicSmemBytes, *out};
+  known[count++ % 32] = Known{device, p.cluster, p.threads, *out};
   return cudaSuccess;
 }
 
-template <typename T, int PT, bool SAME>
+template <typename T, int NV, bool SAME>
 cudaError_t launch_rows(const LossArgs& a, const LossPlan& p, int num_sms, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
-  cfg.blockDim = dim3((unsigned)(p.warps * 32 + 32));
-  cfg.dynamicSmemBytes = (size_t)p.slots * p.chunk * 16;
+  cfg.blockDim = dim3((unsigned)p.threads);
   cfg.stream = s;
   const int in_cluster = p.whole ? kWholeCtas : p.cluster;
   cudaLaunchAttribute attr{};
@@ -620,12 +517,23 @@ cudaError_t launch_rows(const LossArgs& a, const LossPlan& p, int num_sms, cudaS
   // As many clusters as run at once: a persistent grid larger than that would
   // leave its last clusters, and their rows, to a second wave.
   int clusters = 0;
-  cudaError_t e = active_clusters<T, PT, SAME>(p, cfg, num_sms, &clusters);
+  cudaError_t e = active_clusters<T, NV, SAME>(p, cfg, num_sms, &clusters);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)(p.whole ? kWholeCtas : std::min<int64_t>(clusters, a.rows) * p.cluster));
-  e = cudaLaunchKernelEx(&cfg, loss_rows_kernel<T, PT, SAME>, a, p);
+  e = cudaLaunchKernelEx(&cfg, loss_rows_kernel<T, NV, SAME>, a, p);
   note_launch();
   return e;
+}
+
+template <typename T, bool SAME>
+cudaError_t launch_vectors(const LossArgs& a, const LossPlan& p, int num_sms, cudaStream_t s) {
+  switch (p.vectors) {
+    case 1: return launch_rows<T, 1, SAME>(a, p, num_sms, s);
+    case 2: return launch_rows<T, 2, SAME>(a, p, num_sms, s);
+    case 4: return launch_rows<T, 4, SAME>(a, p, num_sms, s);
+    case 8: return launch_rows<T, 8, SAME>(a, p, num_sms, s);
+    default: return launch_rows<T, kMaxVectors, SAME>(a, p, num_sms, s);
+  }
 }
 
 template <typename T>
@@ -639,12 +547,7 @@ cudaError_t launch_typed(const LossArgs& a, int num_sms, cudaStream_t s, bool* s
     return cudaGetLastError();
   }
   const bool same = !a.grad || (reinterpret_cast<uintptr_t>(a.logits) - reinterpret_cast<uintptr_t>(a.grad)) % 16 == 0;
-  if (p.per_thread == 2)
-    return same ? launch_rows<T, 2, true>(a, p, num_sms, s) : launch_rows<T, 2, false>(a, p, num_sms, s);
-  if (p.per_thread == 1)
-    return same ? launch_rows<T, 1, true>(a, p, num_sms, s) : launch_rows<T, 1, false>(a, p, num_sms, s);
-  return same ? launch_rows<T, kPerThread, true>(a, p, num_sms, s)
-              : launch_rows<T, kPerThread, false>(a, p, num_sms, s);
+  return same ? launch_vectors<T, true>(a, p, num_sms, s) : launch_vectors<T, false>(a, p, num_sms, s);
 }
 
 }  // namespace
