@@ -46,6 +46,32 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Two fp32 operations in one instruction: a x + b and a x for a pair, and a sum.
+__device__ __forceinline__ float2 fma2(float2 x, float a, float b) {
+  float2 r;
+  asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %4};\n\tmov.b64 r, {%5, %5};\n\t"
+      "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 x, float a) {
+  float2 r;
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %4};\n\tmul.rn.f32x2 p, p, q;\n\t"
+      "mov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(a));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  float2 r;
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tadd.rn.f32x2 p, p, q;\n\t"
+      "mov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
+}
+
 // The factor from logits to the exponents' units for logits of which the
 // largest is m. Where m log2 e could overflow, two logits that differ at all do
 // so by far more than any exponent, so a quarter of them serves as well (and
@@ -107,23 +133,26 @@ template <>
 struct Vectors<float> {
   static constexpr int kE = 4;
   static constexpr uint32_t kFill = 0xff800000u;  // -inf
-  static __device__ __forceinline__ float get(const uint4& r, int e) {
-    return __uint_as_float(e == 0 ? r.x : e == 1 ? r.y : e == 2 ? r.z : r.w);
+  static __device__ __forceinline__ float2 pair(const uint4& r, int i) {
+    return i == 0 ? make_float2(__uint_as_float(r.x), __uint_as_float(r.y))
+                  : make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
   }
   static __device__ __forceinline__ float max_of(const uint4& r) {
-    return fmaxf(fmaxf(get(r, 0), get(r, 1)), fmaxf(get(r, 2), get(r, 3)));
+    const float2 a = pair(r, 0), b = pair(r, 1);
+    return fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y));
   }
-  static __device__ __forceinline__ uint4 pack(const float* g) {
-    return make_uint4(__float_as_uint(g[0]), __float_as_uint(g[1]), __float_as_uint(g[2]), __float_as_uint(g[3]));
+  static __device__ __forceinline__ uint4 pack(const float2* g) {
+    return make_uint4(__float_as_uint(g[0].x), __float_as_uint(g[0].y), __float_as_uint(g[1].x),
+                      __float_as_uint(g[1].y));
   }
 };
 template <>
 struct Vectors<__nv_bfloat16> {
   static constexpr int kE = 8;
   static constexpr uint32_t kFill = 0xff80ff80u;
-  static __device__ __forceinline__ float get(const uint4& r, int e) {
-    const uint32_t w = e < 2 ? r.x : e < 4 ? r.y : e < 6 ? r.z : r.w;
-    return __uint_as_float((e & 1) ? (w & 0xffff0000u) : (w << 16));
+  static __device__ __forceinline__ float2 pair(const uint4& r, int i) {
+    const uint32_t w = i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w;
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   }
   static __device__ __forceinline__ __nv_bfloat162 both(uint32_t w) {
     return *reinterpret_cast<const __nv_bfloat162*>(&w);
@@ -132,12 +161,12 @@ struct Vectors<__nv_bfloat16> {
     const __nv_bfloat162 m = __hmax2(__hmax2(both(r.x), both(r.y)), __hmax2(both(r.z), both(r.w)));
     return fmaxf(__low2float(m), __high2float(m));
   }
-  static __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  static __device__ __forceinline__ uint32_t pack2(float2 x) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x.x, x.y);
     return *reinterpret_cast<const uint32_t*>(&v);
   }
-  static __device__ __forceinline__ uint4 pack(const float* g) {
-    return make_uint4(pack2(g[0], g[1]), pack2(g[2], g[3]), pack2(g[4], g[5]), pack2(g[6], g[7]));
+  static __device__ __forceinline__ uint4 pack(const float2* g) {
+    return make_uint4(pack2(g[0]), pack2(g[1]), pack2(g[2]), pack2(g[3]));
   }
 };
 
@@ -225,20 +254,23 @@ __global__ void __launch_bounds__(kMaxThreads, 2) loss_rows_kernel(LossArgs a, L
     *target = (int)id;
     return live;
   };
-  uint4 raw[NV];                       // this thread's vectors: tid + n threads of the slice
+  // This thread's vectors: j0 + 32 n of the slice, each warp a run of 32 NV.
+  const int j0 = warp * 32 * NV + lane;
+  uint4 raw[NV];
   float edge = -INFINITY, xt = 0.0f;   // its edge element; the target's logit
-  auto load_singles = [&](int row, int target) {
+  // Rows of whole vectors all begin alike.
+  const bool ragged = vocab % kE != 0;
+  const RowShape<T> first_shape(logits, vocab);
+  auto shape_of = [&](int row) { return ragged ? RowShape<T>(logits + (int64_t)row * vocab, vocab) : first_shape; };
+  auto load_singles = [&](int row, const RowShape<T>& shape, int target) {
     const T* c = logits + (int64_t)row * vocab;
-    const RowShape<T> shape(c, vocab);
     edge = rank == 0 && tid < shape.edges ? to_f32(c[shape.edge(tid)]) : -INFINITY;
     xt = to_f32(c[target]);
   };
-  // Where a vector is not in the slice its registers hold -inf; only rows that
-  // do not all begin alike change which those are.
-  const bool ragged = vocab % kE != 0;
+  // Where a vector is not in the slice its registers hold -inf.
   auto load = [&](const uint4* from, int left, int n) {
-    if (n * threads < left)
-      raw[n] = __ldcs(from + n * threads);
+    if (32 * n < left)
+      raw[n] = __ldcs(from + 32 * n);
     else if (ragged)
       raw[n] = make_uint4(Vectors<T>::kFill, Vectors<T>::kFill, Vectors<T>::kFill, Vectors<T>::kFill);
   };
@@ -248,12 +280,12 @@ __global__ void __launch_bounds__(kMaxThreads, 2) loss_rows_kernel(LossArgs a, L
   bool live = look_up(i, &t, &w);
   if (live) {
     const T* c = logits + (int64_t)i * vocab;
-    const RowShape<T> shape(c, vocab);
-    const uint4* from = reinterpret_cast<const uint4*>(c + shape.head) + (int64_t)rank * p.slice + tid;
-    const int left = slice_vectors(p, shape.vecs, rank) - tid;
+    const RowShape<T> shape = shape_of(i);
+    const uint4* from = reinterpret_cast<const uint4*>(c + shape.head) + rank * p.slice + j0;
+    const int left = slice_vectors(p, shape.vecs, rank) - j0;
 #pragma unroll
     for (int n = 0; n < NV; ++n) load(from, left, n);
-    load_singles(i, t);
+    load_singles(i, shape, t);
   }
   const double inv_n = inverse_total(a, sums, false);
   __syncthreads();
@@ -266,31 +298,31 @@ __global__ void __launch_bounds__(kMaxThreads, 2) loss_rows_kernel(LossArgs a, L
     int next_t = 0;
     float next_w = 0.0f;
     const bool next_live = look_up(next, &next_t, &next_w);
-    const RowShape<T> shape(logits + (int64_t)i * vocab, vocab);
+    const RowShape<T> shape = shape_of(i);
     const int count = slice_vectors(p, shape.vecs, rank);
-    const int left = grads ? count - tid : 0;
+    const int left = grads ? count - j0 : 0;
     T* g = grads ? grads + (int64_t)i * vocab : nullptr;
-    T* to = g + shape.head + ((int64_t)rank * p.slice + tid) * kE;
+    T* to = g + shape.head + (rank * p.slice + j0) * kE;
     const T* cn = logits + (int64_t)next * vocab;
-    const RowShape<T> next_shape(cn, vocab);
-    const uint4* from = reinterpret_cast<const uint4*>(cn + next_shape.head) + (int64_t)rank * p.slice + tid;
-    const int next_left = next_live ? slice_vectors(p, next_shape.vecs, rank) - tid : 0;
+    const RowShape<T> next_shape = shape_of(next);
+    const uint4* from = reinterpret_cast<const uint4*>(cn + next_shape.head) + rank * p.slice + j0;
+    const int next_left = next_live ? slice_vectors(p, next_shape.vecs, rank) - j0 : 0;
     if (!live) {
       if (rank == 0 && tid == 0) a.row_losses[i] = 0.0f;
       if (g && rank == 0 && tid < shape.edges) g[shape.edge(tid)] = from_f32<T>(0.0f);
 #pragma unroll
       for (int n = 0; n < NV; ++n) {
-        if (n * threads < left) {
+        if (32 * n < left) {
           if (SAME) {
-            __stcs(reinterpret_cast<uint4*>(to) + n * threads, make_uint4(0u, 0u, 0u, 0u));
+            __stcs(reinterpret_cast<uint4*>(to) + 32 * n, make_uint4(0u, 0u, 0u, 0u));
           } else {
 #pragma unroll
-            for (int e = 0; e < kE; ++e) to[n * threads * kE + e] = from_f32<T>(0.0f);
+            for (int e = 0; e < kE; ++e) to[32 * n * kE + e] = from_f32<T>(0.0f);
           }
         }
         load(from, next_left, n);
       }
-      if (next_live) load_singles(next, next_t);
+      if (next_live) load_singles(next, next_shape, next_t);
     } else {
       // Pass 1. A thread of -inf alone keeps m = -inf and sums zeros (or NaN).
       float m = edge;
@@ -299,12 +331,15 @@ __global__ void __launch_bounds__(kMaxThreads, 2) loss_rows_kernel(LossArgs a, L
       float s;
       {
         const float unit = unit_for(m), ref = reference(m);
-        float part[4] = {ex2(fmaf(edge, unit, -ref)), 0.0f, 0.0f, 0.0f};
+        float2 part[2] = {make_float2(ex2(fmaf(edge, unit, -ref)), 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
         for (int n = 0; n < NV; ++n)
 #pragma unroll
-          for (int e = 0; e < kE; ++e) part[e & 3] += ex2(fmaf(Vectors<T>::get(raw[n], e), unit, -ref));
-        s = (part[0] + part[1]) + (part[2] + part[3]);
+          for (int e = 0; e < kE / 2; ++e) {
+            const float2 x = fma2(Vectors<T>::pair(raw[n], e), unit, -ref);
+            part[e & 1] = add2(part[e & 1], make_float2(ex2(x.x), ex2(x.y)));
+          }
+        s = (part[0].x + part[0].y) + (part[1].x + part[1].y);
       }
       float top = m;
 #pragma unroll
@@ -327,26 +362,27 @@ __global__ void __launch_bounds__(kMaxThreads, 2) loss_rows_kernel(LossArgs a, L
       }
       __syncwarp();
       const float row_xt = xt, row_edge = edge;
-      if (next_live) load_singles(next, next_t);
+      if (next_live) load_singles(next, next_shape, next_t);
       // Whether the target is in one of this thread's vectors.
       const int at = t - shape.head, vec = at >= 0 ? at / kE - rank * p.slice : -1;
-      const bool own_target = vec >= 0 && vec < count && vec % threads == tid;
+      const bool own_target = vec >= 0 && vec < count && vec / (32 * NV) == warp && vec % 32 == lane;
       const float scale = (float)((double)w * inv_n);
       mbar_wait_cluster(&met_bar[parity], met_phase, ctl);
-      // Each warp for itself, a lane for up to four pairs.
-      float2 met[kMaxCluster * kMaxWarps / 32];
+      // Each warp for itself. Without NaN, which is orderable above all: a
+      // warp's maximum is NaN only where it has no number at all.
+      const int met = ranks * warps;
       uint32_t high = 0u;
-#pragma unroll
-      for (int k = 0; k < kMaxCluster * kMaxWarps / 32; ++k) {
-        met[k] = lane + 32 * k < ranks * warps ? pairs[parity][lane + 32 * k] : make_float2(-INFINITY, 0.0f);
-        // Without NaN (orderable above all): a warp's maximum is NaN only where it has no number at all.
-        high = max(high, met[k].x == met[k].x ? orderable_bits(met[k].x) : 0u);
+      for (int k = lane; k < met; k += 32) {
+        const float x = pairs[parity][k].x;
+        high = max(high, x == x ? orderable_bits(x) : 0u);
       }
       high = __reduce_max_sync(0xffffffffu, high);
-      m = __uint_as_float((high & 0x80000000u) ? high & 0x7fffffffu : ~high);
+      m = high == 0u ? -INFINITY : __uint_as_float((high & 0x80000000u) ? high & 0x7fffffffu : ~high);
       s = 0.0f;
-#pragma unroll
-      for (int k = 0; k < kMaxCluster * kMaxWarps / 32; ++k) s += rescaled(met[k].y, met[k].x, m);
+      for (int k = lane; k < met; k += 32) {
+        const float2 q = pairs[parity][k];
+        s += rescaled(q.y, q.x, m);
+      }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       parity ^= 1;
@@ -366,15 +402,21 @@ __global__ void __launch_bounds__(kMaxThreads, 2) loss_rows_kernel(LossArgs a, L
       // Pass 2.
 #pragma unroll
       for (int n = 0; n < NV; ++n) {
-        if (n * threads < left) {
-          float x[kE];
+        if (32 * n < left) {
+          float2 x[kE / 2];
 #pragma unroll
-          for (int e = 0; e < kE; ++e) x[e] = ex2(fmaf(Vectors<T>::get(raw[n], e), unit, -ref)) * factor;
+          for (int e = 0; e < kE / 2; ++e) {
+            x[e] = fma2(Vectors<T>::pair(raw[n], e), unit, -ref);
+            x[e] = mul2(make_float2(ex2(x[e].x), ex2(x[e].y)), factor);
+          }
           if (SAME) {
-            __stcs(reinterpret_cast<uint4*>(to) + n * threads, Vectors<T>::pack(x));
+            __stcs(reinterpret_cast<uint4*>(to) + 32 * n, Vectors<T>::pack(x));
           } else {
 #pragma unroll
-            for (int e = 0; e < kE; ++e) to[n * threads * kE + e] = from_f32<T>(x[e]);
+            for (int e = 0; e < kE / 2; ++e) {
+              to[32 * n * kE + 2 * e] = from_f32<T>(x[e].x);
+              to[32 * n * kE + 2 * e + 1] = from_f32<T>(x[e].y);
+            }
           }
         }
         load(from, next_left, n);
