@@ -26,7 +26,6 @@
 //                copy (67 us for 32 x 8 rows of 151936 bf16).
 #include <algorithm>
 #include <cmath>
-#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -38,17 +37,15 @@ namespace {
 
 constexpr int kBlock = 512;        // ids; the unit of parts and stretches, with a place of its own in the lists
 constexpr int kListThreads = 1024;
-constexpr int kRounds = 4;         // words of 32 ids per thread of list_kernel, at most
-constexpr int kMaxPart = kListThreads * kRounds * 32;
+constexpr int kRounds = 2;         // words of 32 ids per thread of list_kernel, at most
+constexpr int kMaxPart = kListThreads * kRounds * 32;  // 16-bit places in its list
 constexpr int kListSmem = 222 * 1024;
 constexpr int kAhead = 8;          // history ids in flight per thread
-constexpr int kCopyThreads = 512;
-constexpr int kMaxStretch = 32768;
+constexpr int kCopyThreads = 256;
+constexpr int kCopyCtas = 4;       // per SM
+constexpr int kMaxStretch = 16384;
 constexpr int kInFlight = 4;       // vectors, or listed logits, under way per thread
 constexpr int kRows = 8;           // rows copied before their listed logits are worked out
-template <int N>
-using Int = std::integral_constant<int, N>;
-
 constexpr uint32_t kFlag = 0x80000000u;  // of an entry's id: biased; of its count: in the prompt
 
 // The sizes of both kernels and the places in the scratch, for one call.
@@ -120,6 +117,7 @@ __global__ void __launch_bounds__(kListThreads, 1) list_kernel(ConstrainArgs a, 
   uint32_t* in_block = smem + words;     // drafted in this block
   C* count = reinterpret_cast<C*>(smem + 2 * words);
   C* slot = count + p.part;              // last bias entry + 1, where there are biases
+  uint16_t* list = reinterpret_cast<uint16_t*>(slot + (p.has_bias ? p.part : 0));  // what there is, in order
   // The first ids of the history are read while the cells are cleared, before
   // its length is known: its buffer covers them.
   const int cap = a.history ? (int)a.history_cap : 0;
@@ -200,17 +198,22 @@ __global__ void __launch_bounds__(kListThreads, 1) list_kernel(ConstrainArgs a, 
     if (w < words) {
       word[r] = in_prompt[w] | in_block[w];
       constexpr int kPer = 16 / sizeof(C);  // cells of 16 bytes
+      // Neighbouring lanes begin at different places of their 32 cells, which
+      // lie a multiple of the banks apart.
       auto look = [&](const C* cells) {
 #pragma unroll
         for (int i = 0; i < 32 / kPer; ++i) {
-          const uint4 x = *reinterpret_cast<const uint4*>(cells + w * 32 + i * kPer);
+          const int at = (i + lane / (8 / (32 / kPer > 8 ? 8 : 32 / kPer))) % (32 / kPer) * kPer;
+          const uint4 x = *reinterpret_cast<const uint4*>(cells + w * 32 + at);
           if (x.x | x.y | x.z | x.w) {
+            uint32_t some = 0u;
 #pragma unroll
             for (int e = 0; e < kPer; ++e) {
               const uint32_t v = sizeof(C) == 4 ? (e == 0 ? x.x : e == 1 ? x.y : e == 2 ? x.z : x.w)
                                                 : ((e < 2 ? x.x : e < 4 ? x.y : e < 6 ? x.z : x.w) >> (16 * (e & 1))) & 0xffffu;
-              if (v) word[r] |= 1u << (i * kPer + e);
+              if (v) some |= 1u << e;
             }
+            word[r] |= some << at;
           }
         }
       };
@@ -245,34 +248,29 @@ __global__ void __launch_bounds__(kListThreads, 1) list_kernel(ConstrainArgs a, 
   }
   __syncthreads();
 
-  const int blocks = p.part / kBlock;
+  const int blocks = p.part / kBlock, total = totals[kRounds * warps];
   const int64_t which = b * p.parts + part;
   uint32_t* before = plane<uint32_t>(a, p.before) + which * (blocks + 1);
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const int w = (r * warps + warp) * 32 + lane;
+    int at = totals[r * warps + warp] + mine[r];
+    if (w < words && w % (kBlock / 32) == 0) before[w / (kBlock / 32)] = (uint32_t)at;
+    for (uint32_t bits = word[r]; bits; bits &= bits - 1u) list[at++] = (uint16_t)(w * 32 + __ffs((int)bits) - 1);
+  }
+  if (tid == 0) before[blocks] = (uint32_t)total;
+  __syncthreads();
   uint32_t* ids = plane<uint32_t>(a, p.ids) + which * p.entries;
   uint32_t* counts = plane<uint32_t>(a, p.counts) + which * p.entries;
   float* biases = plane<float>(a, p.biases) + which * p.entries;
   const float* bias = a.bias_values + b * a.bias_stride;
-#pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
-    const int w0 = (r * warps + warp) * 32, base = totals[r * warps + warp];
-    if (w0 + lane < words && (w0 + lane) % (kBlock / 32) == 0)
-      before[(w0 + lane) / (kBlock / 32)] = (uint32_t)(base + mine[r]);
-    // The warp's words one after another, a lane per id.
-    uint32_t some = __ballot_sync(0xffffffffu, word[r] != 0u);
-    for (; some; some &= some - 1u) {
-      const int from = __ffs((int)some) - 1;
-      const uint32_t bits = __shfl_sync(0xffffffffu, word[r], from);
-      const int at = base + __shfl_sync(0xffffffffu, mine[r], from) + __popc(bits & ((1u << lane) - 1u));
-      if ((bits >> lane) & 1u) {
-        const int l = (w0 + from) * 32 + lane;
-        const uint32_t entry = p.has_bias ? (uint32_t)slot[l] : 0u;
-        ids[at] = (uint32_t)(c0 + l) | (entry ? kFlag : 0u);
-        counts[at] = (uint32_t)count[l] | (bit(in_prompt, l) ? kFlag : 0u);
-        if (entry) biases[at] = bias[entry - 1u];
-      }
-    }
+  for (int e = tid; e < total; e += threads) {
+    const int l = (int)list[e];
+    const uint32_t entry = p.has_bias ? (uint32_t)slot[l] : 0u;
+    ids[e] = (uint32_t)(c0 + l) | (entry ? kFlag : 0u);
+    counts[e] = (uint32_t)count[l] | (bit(in_prompt, l) ? kFlag : 0u);
+    if (entry) biases[e] = bias[entry - 1u];
   }
-  if (tid == 0) before[blocks] = (uint32_t)totals[kRounds * warps];
   if (bad) report_status(a.status, DSPARK_STATUS_TOKEN_RANGE);
 }
 
@@ -352,73 +350,35 @@ __device__ __forceinline__ unsigned long long max_key(unsigned long long a, unsi
 
 // ALIGNED: every row starts at a 16-byte address, in and out.
 template <typename T, bool ALIGNED>
-__global__ void __launch_bounds__(kCopyThreads, 2) copy_kernel(ConstrainArgs a, ConstrainPlan p) {
+__global__ void __launch_bounds__(kCopyThreads, kCopyCtas) copy_kernel(ConstrainArgs a, ConstrainPlan p) {
   constexpr int kE = Vec<T>::kE;
   extern __shared__ __align__(16) uint32_t touched[];  // one bit per id of the stretch: listed
   __shared__ int drafted[kRows];  // the tokens drafted after each of the rows (-1: none)
   __shared__ unsigned long long warp_key[kRows][kCopyThreads / 32], listed_key[kRows];
+  __shared__ float warp_best[kRows][kCopyThreads / 32];  // greedy: the warp's largest value
+  __shared__ int warp_at[kRows][kCopyThreads / 32];      // and the first id of its vector, or ~ the id of a single
   __shared__ bool last;
-  const int tid = (int)threadIdx.x, lane = tid & 31, threads = (int)blockDim.x;
+  const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = (int)blockDim.x;
   const int64_t b = blockIdx.x / p.stretches;
   const int stretch = (int)(blockIdx.x % p.stretches);
   const int64_t c0 = (int64_t)stretch * p.stretch, rows = a.block;
   const int n = (int)min((int64_t)p.stretch, a.vocab - c0);
   const int words = p.stretch / 32, mask_last = (n + 31) / 32 - 1;
   const bool keyed = a.tokens != nullptr;
+  constexpr int kNone = 0x7fffffff;
   auto score = [&](float y, int64_t k, int l) {
     const uint32_t v = (uint32_t)(c0 + l);
     return pack_key(y / a.temperature + noise_for(a.seed, (uint32_t)b, (uint32_t)(a.draft_first + k), v), v);
   };
-
-  // Rows are walked by pointers. A row's stretch is `head` elements before the
-  // first 16-byte address, whole vectors, and what is left.
   const T* const in0 = static_cast<const T*>(a.in) + b * a.in_batch + c0;
   T* const out0 = static_cast<T*>(a.out) + b * a.out_batch + c0;
   const uint32_t* const mask0 = a.allowed ? a.allowed + b * a.allowed_batch + (c0 >> 5) : nullptr;
-  auto head_of = [&](const T* in, const T* out) {
-    if (ALIGNED) return 0;
-    const int past = (int)((reinterpret_cast<uintptr_t>(in) / sizeof(T)) % kE);
-    const bool same = (reinterpret_cast<uintptr_t>(in) - reinterpret_cast<uintptr_t>(out)) % 16 == 0;
-    return same ? min(past ? kE - past : 0, n) : n;  // all single where the output's vectors lie elsewhere
-  };
-  // The thread's vectors of all rows in one stream: vector tid + q threads of
-  // a row, then the next q below `per_row`, then the next row. kInFlight of
-  // them are loaded ahead. A vector's mask words are shifted when used: a use
-  // here would wait for the load.
-  const int per_row = max(1, (n / kE + threads - 1) / threads);
-  struct Loaded {
-    uint4 raw;
-    uint32_t lo, hi;
-  };
-  Loaded ahead[kInFlight];
-  const T* load_in = in0;
-  const T* load_out = out0;
-  const uint32_t* load_mask = mask0;
-  int64_t load_left = rows;
-  int load_q = per_row, load_j = tid, load_head = head_of(in0, out0);  // load_q counts down
-  auto load = [&](Loaded& to) {
-    if (load_left <= 0) return;
-    if (load_j < (n - load_head) / kE) {
-      to.raw = __ldcs(reinterpret_cast<const uint4*>(load_in + load_head) + load_j);
-      if (load_mask) {
-        const int w = (load_head + load_j * kE) >> 5;
-        to.lo = load_mask[w];
-        if (!ALIGNED) to.hi = w < mask_last ? load_mask[w + 1] : 0u;
-      }
-    }
-    load_j += threads;
-    if (--load_q == 0) {
-      load_q = per_row;
-      load_j = tid;
-      --load_left;
-      load_in += a.in_row;
-      load_out += a.out_row;
-      load_head = head_of(load_in, load_out);
-      if (load_mask) load_mask += a.allowed_row;
-    }
-  };
-#pragma unroll
-  for (int u = 0; u < kInFlight; ++u) load(ahead[u]);
+  // The first rows come into L2 while the lists are made.
+  for (int64_t k = 0; k < min(rows, (int64_t)kRows); ++k) {
+    const char* row = reinterpret_cast<const char*>(in0 + k * a.in_row);
+    for (int at = tid * 128; at < n * (int)sizeof(T); at += threads * 128)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(row + at));
+  }
 
   // What is listed in the stretch: a run of entries in each part that it meets.
   for (int i = tid; i < words; i += threads) touched[i] = 0u;
@@ -439,14 +399,36 @@ __global__ void __launch_bounds__(kCopyThreads, 2) copy_kernel(ConstrainArgs a, 
   const float* biases = plane<float>(a, p.biases);
   __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the lists are there
-  if (keyed) {
-    for (int part = part0; part < part1; ++part) {
+  // One entry after another over the runs; each thread keeps its first.
+  int entries = 0;
+  for (int part = part0; part < part1; ++part) {
+    int64_t from, to;
+    run(part, &from, &to);
+    entries += (int)(to - from);
+  }
+  auto entry_at = [&](int e, uint32_t* id, uint32_t* counted, float* beta) {
+    for (int part = part0;; ++part) {
       int64_t from, to;
       run(part, &from, &to);
-      for (int64_t e = from + tid; e < to; e += threads) {
-        const int l = (int)((int64_t)(ids[e] & ~kFlag) - c0);
-        atomicOr(&touched[l >> 5], 1u << (l & 31));
+      if (e < (int)(to - from) || part == part1 - 1) {
+        *id = ids[from + e];
+        *counted = counts[from + e];
+        *beta = p.has_bias ? biases[from + e] : 0.0f;  // of no meaning where the id has no flag
+        return;
       }
+      e -= (int)(to - from);
+    }
+  };
+  uint32_t my_id = 0u, my_count = 0u;
+  float my_beta = 0.0f;
+  if (tid < entries) entry_at(tid, &my_id, &my_count, &my_beta);
+  if (keyed) {
+    for (int e = tid; e < entries; e += threads) {
+      uint32_t id = my_id, counted;
+      float beta;
+      if (e != tid) entry_at(e, &id, &counted, &beta);
+      const int l = (int)((id & ~kFlag) - (uint32_t)c0);
+      atomicOr(&touched[l >> 5], 1u << (l & 31));
     }
     __syncthreads();
   }
@@ -458,168 +440,184 @@ __global__ void __launch_bounds__(kCopyThreads, 2) copy_kernel(ConstrainArgs a, 
       const int64_t id = draft && k0 + tid < rows - 1 ? draft[k0 + tid] : -1;
       drafted[tid] = id >= 0 && id < a.vocab ? (int)id : -1;
     }
+
+    // The copy. Greedy keys: the largest value so far and the first id of its
+    // vector; a single element has the complement of its id. A row of -inf
+    // alone keeps the first threads' own ids, of which the lowest wins. Listed
+    // logits stand aside as -inf.
     const T* in = in0 + k0 * a.in_row;
     T* out = out0 + k0 * a.out_row;
     const uint32_t* mask = mask0 ? mask0 + k0 * a.allowed_row : nullptr;
-
-    // The copy. Greedy keys: the largest value so far, the vector (and its
-    // first id) that holds it; a single element is a vector of its own. A row
-    // of -inf alone keeps the first threads' own ids, of which the lowest
-    // wins. Listed logits stand aside as -inf.
-    float best = -INFINITY;
-    int best_at = tid < n ? tid : -1;
-    uint4 best_vec = make_uint4(0u, 0u, 0u, 0u);
-    bool best_single = true;
-    unsigned long long key = 0ull;
-    // Strictly larger, or the first NaN: ids rise, so equal values keep the lower one.
-    auto better = [&](float y) { return y > best || (y != y && best == best); };
-    auto single = [&](int64_t k, int l) {
-      const T y = !mask || bit(mask, l) ? in[l] : from_f32<T>(-INFINITY);
-      out[l] = y;
-      if (!keyed || bit(touched, l)) return;
-      if (!a.greedy) {
-        key = max_key(key, score(to_f32(y), k, l));
-      } else if (better(to_f32(y))) {
-        best = to_f32(y);
-        best_at = l;
-        best_single = true;
+    for (int r = 0; r < group; ++r) {
+      float best = -INFINITY;
+      int best_at = tid < n ? ~tid : kNone;
+      unsigned long long key = 0ull;
+      // Strictly larger, or the first NaN: ids rise, so equal values keep the lower one.
+      auto better = [&](float y) { return y > best || (y != y && best == best); };
+      auto single = [&](int l) {
+        const T y = !mask || bit(mask, l) ? in[l] : from_f32<T>(-INFINITY);
+        out[l] = y;
+        if (!keyed || bit(touched, l)) return;
+        if (!a.greedy) {
+          key = max_key(key, score(to_f32(y), k0 + r, l));
+        } else if (better(to_f32(y))) {
+          best = to_f32(y);
+          best_at = ~l;
+        }
+      };
+      // Elements before the first 16-byte address, vectors, and what is left;
+      // all single where the output's vectors lie elsewhere.
+      int head = 0;
+      if (!ALIGNED) {
+        const int past = (int)((reinterpret_cast<uintptr_t>(in) / sizeof(T)) % kE);
+        const bool same = (reinterpret_cast<uintptr_t>(in) - reinterpret_cast<uintptr_t>(out)) % 16 == 0;
+        head = same ? min(past ? kE - past : 0, n) : n;
+        for (int l = tid; l < head; l += threads) single(l);
       }
-    };
-    int r = 0, q = per_row, j = tid, head = head_of(in, out);  // q counts down
-    while (r < group) {
+      const int vecs = (n - head) / kE;
+      const uint4* from = reinterpret_cast<const uint4*>(in + head);
+      uint4* to = reinterpret_cast<uint4*>(out + head);
+      for (int j0 = tid; j0 < vecs; j0 += threads * kInFlight) {
+        uint4 raw[kInFlight];
+        uint32_t lo[kInFlight], hi[kInFlight];
 #pragma unroll
-      for (int u = 0; u < kInFlight; ++u) {
-        if (r >= group) break;
-        if (!ALIGNED && q == per_row)
-          for (int l = tid; l < head; l += threads) single(k0 + r, l);
-        const int l = head + j * kE;
-        if (j < (n - head) / kE) {
-          uint4 raw = ahead[u].raw;
-          if (mask)
-            raw = Vec<T>::masked(raw, ALIGNED ? ahead[u].lo >> (l & 31)
-                                              : __funnelshift_r(ahead[u].lo, ahead[u].hi, l & 31));
-          __stcs(reinterpret_cast<uint4*>(out + head) + j, raw);
-          if (keyed) {
-            raw = Vec<T>::masked(raw, ~bits_at<ALIGNED>(touched, l, words - 1));
-            if (a.greedy) {
-              const float top = Vec<T>::max_of(raw);
-              if (better(top)) {
-                best = top;
-                best_at = l;
-                best_vec = raw;
-                best_single = false;
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < kE; ++e) key = max_key(key, score(Vec<T>::get(raw, e), k0 + r, l + e));
+        for (int u = 0; u < kInFlight; ++u) {
+          const int j = j0 + u * threads;
+          if (j < vecs) {
+            raw[u] = __ldcs(from + j);
+            if (mask) {
+              const int w = (head + j * kE) >> 5;
+              lo[u] = mask[w];
+              if (!ALIGNED) hi[u] = w < mask_last ? mask[w + 1] : 0u;
             }
           }
         }
-        load(ahead[u]);
-        j += threads;
-        if (--q == 0) {
-          for (int t = head + (n - head) / kE * kE + tid; t < n; t += threads) single(k0 + r, t);
-          if (keyed) {
-            if (a.greedy && best_at >= 0) {
-              if (!best_single) {
-                int first = kE;
 #pragma unroll
-                for (int e = kE - 1; e >= 0; --e) {
-                  const float y = Vec<T>::get(best_vec, e);
-                  if (y == best || (y != y && best != best)) first = e;
+        for (int u = 0; u < kInFlight; ++u) {
+          const int j = j0 + u * threads, l = head + j * kE;
+          if (j < vecs) {
+            if (mask) raw[u] = Vec<T>::masked(raw[u], ALIGNED ? lo[u] >> (l & 31) : __funnelshift_r(lo[u], hi[u], l & 31));
+            __stcs(to + j, raw[u]);
+            if (keyed) {
+              const uint32_t aside = bits_at<ALIGNED>(touched, l, words - 1) & ((1u << kE) - 1u);
+              if (aside) raw[u] = Vec<T>::masked(raw[u], ~aside);
+              if (a.greedy) {
+                const float top = Vec<T>::max_of(raw[u]);
+                if (better(top)) {
+                  best = top;
+                  best_at = l;
                 }
-                best_at += first;
+              } else {
+#pragma unroll
+                for (int e = 0; e < kE; ++e) key = max_key(key, score(Vec<T>::get(raw[u], e), k0 + r, l + e));
               }
-              key = pack_key(best, (uint32_t)(c0 + best_at));
             }
-            // The warp's largest key: the larger high word, then the larger low one.
-            const uint32_t high = __reduce_max_sync(0xffffffffu, (uint32_t)(key >> 32));
-            const uint32_t low = __reduce_max_sync(0xffffffffu, (uint32_t)(key >> 32) == high ? (uint32_t)key : 0u);
-            if (lane == 0) warp_key[r][tid >> 5] = ((unsigned long long)high << 32) | low;
-            best = -INFINITY;
-            best_at = tid < n ? tid : -1;
-            best_single = true;
-            key = 0ull;
           }
-          q = per_row;
-          j = tid;
-          ++r;
-          in += a.in_row;
-          out += a.out_row;
-          if (mask) mask += a.allowed_row;
-          head = head_of(in, out);
         }
       }
+      for (int l = head + vecs * kE + tid; l < n; l += threads) single(l);
+      if (keyed && a.greedy) {
+        // The warp's largest value, of equal ones the first; which element of
+        // its vector is found for all rows together.
+        const uint32_t order = best_at != kNone ? orderable_bits(best) : 0u, top = __reduce_max_sync(0xffffffffu, order);
+        const int id = best_at < 0 ? ~best_at : best_at;
+        const int first = __reduce_min_sync(0xffffffffu, order == top ? id : kNone);
+        if (order == top && id == first) {
+          warp_best[r][warp] = best;
+          warp_at[r][warp] = best_at;
+        }
+      } else if (keyed) {
+        // The warp's largest key: the larger high word, then the larger low one.
+        const uint32_t high = __reduce_max_sync(0xffffffffu, (uint32_t)(key >> 32));
+        const uint32_t low = __reduce_max_sync(0xffffffffu, (uint32_t)(key >> 32) == high ? (uint32_t)key : 0u);
+        if (lane == 0) warp_key[r][warp] = ((unsigned long long)high << 32) | low;
+      }
+      in += a.in_row;
+      out += a.out_row;
+      if (mask) mask += a.allowed_row;
     }
     __syncthreads();
+    if (keyed && a.greedy && tid < group * (threads >> 5)) {
+      const int row = tid / (threads >> 5), w = tid % (threads >> 5), at = warp_at[row][w];
+      unsigned long long own = 0ull;
+      if (at != kNone) {
+        const float top = warp_best[row][w];
+        int id = ~at;
+        if (at >= 0) {
+          const uint4 vec = *reinterpret_cast<const uint4*>(out0 + (k0 + row) * a.out_row + at);
+          const uint32_t aside = bits_at<ALIGNED>(touched, at, words - 1);
+          int first = 0;
+#pragma unroll
+          for (int e = kE - 1; e >= 0; --e) {
+            const float y = Vec<T>::get(vec, e);
+            if ((y == top || (y != y && top != top)) && !((aside >> e) & 1u)) first = e;
+          }
+          id = at + first;
+        }
+        own = pack_key(top, (uint32_t)(c0 + id));
+      }
+      warp_key[row][w] = own;
+    }
+    if (keyed) __syncthreads();  // before listed logits change the vectors just looked at
 
-    // The listed logits of these rows, after the copies of them. What the copy
-    // left in place of a masked one stays; in place, an allowed one's input is
-    // what the copy wrote. A step takes EN entries and RN of their rows.
-    auto listed = [&](auto entries_per_step, auto rows_per_step) {
-      constexpr int EN = decltype(entries_per_step)::value, RN = decltype(rows_per_step)::value;
-      for (int part = part0; part < part1; ++part) {
-        int64_t from, to;
-        run(part, &from, &to);
-        for (int64_t e0 = from + tid; e0 < to; e0 += threads * EN) {
-          uint32_t id[EN], counted[EN];
+    // The listed logits of these rows, after the copies of them, a thread for
+    // each entry and all rows. What the copy left in place of a masked one
+    // stays; in place, an allowed one's input is what the copy wrote.
+    for (int e = tid; e < entries; e += threads) {
+      uint32_t id = my_id, counted = my_count;
+      float beta = my_beta;
+      if (e != tid) entry_at(e, &id, &counted, &beta);
+      const int token = (int)(id & ~kFlag), l = (int)((uint32_t)token - (uint32_t)c0);
+      T x[kRows];
+      uint32_t allowed = 0u;
+      const T* rin = in0 + k0 * a.in_row + l;
 #pragma unroll
-          for (int u = 0; u < EN; ++u) {
-            const int64_t e = min(e0 + u * threads, to - 1);
-            id[u] = ids[e];
-            counted[u] = counts[e];
-          }
-          if (draft && k0 > 0) {  // drafted in earlier groups
-            for (int64_t d = 0; d < k0; ++d) {
-              const int64_t t = draft[d];
-#pragma unroll
-              for (int u = 0; u < EN; ++u) counted[u] += t == (int64_t)(id[u] & ~kFlag) ? 1u : 0u;
-            }
-          }
-          for (int g0 = 0; g0 < group; g0 += RN) {
-            T x[EN][RN];
-            uint32_t word[EN][RN];
-#pragma unroll
-            for (int u = 0; u < EN; ++u)
-#pragma unroll
-              for (int g = 0; g < RN; ++g) {
-                const int l = (int)((int64_t)(id[u] & ~kFlag) - c0);
-                const int64_t k = k0 + min(g0 + g, group - 1);
-                x[u][g] = in0[k * a.in_row + l];
-                word[u][g] = mask0 ? mask0[k * a.allowed_row + (l >> 5)] : ~0u;
-              }
-#pragma unroll
-            for (int u = 0; u < EN; ++u) {
-              const float beta = (id[u] & kFlag) ? biases[min(e0 + u * threads, to - 1)] : 0.0f;
-#pragma unroll
-              for (int g = 0; g < RN; ++g) {
-                const int l = (int)((int64_t)(id[u] & ~kFlag) - c0), row = g0 + g;
-                if (row >= group || e0 + u * threads >= to) break;
-                const uint32_t times = counted[u] & ~kFlag;
-                if (drafted[row] == (int)(id[u] & ~kFlag)) counted[u] += 1u;  // from the next row on
-                if (!((word[u][g] >> (l & 31)) & 1u)) continue;
-                float f = to_f32(x[u][g]);
-                if (times || ((counted[u] & kFlag) != 0u)) f = f > 0.0f ? __fdiv_rn(f, rho) : __fmul_rn(f, rho);
-                if (times) f = __fsub_rn(__fsub_rn(f, __fmul_rn(freq, (float)times)), pres);
-                if (id[u] & kFlag) f = __fadd_rn(f, beta);
-                const T y = from_f32<T>(f);
-                out0[(k0 + row) * a.out_row + l] = y;
-                if (keyed) {
-                  const unsigned long long own =
-                      a.greedy ? pack_key(to_f32(y), (uint32_t)(c0 + l)) : score(to_f32(y), k0 + row, l);
-                  if (own > *reinterpret_cast<volatile unsigned long long*>(&listed_key[row]))
-                    atomicMax(&listed_key[row], own);
-                }
-              }
-            }
-          }
+      for (int g = 0; g < kRows; ++g) {
+        x[g] = from_f32<T>(0.0f);
+        if (g < group) {
+          x[g] = *rin;
+          rin += a.in_row;
         }
       }
-    };
-    if (group >= 3)
-      listed(Int<1>{}, Int<kInFlight>{});
-    else
-      listed(Int<kInFlight>{}, Int<1>{});
+      if (mask0) {
+        const uint32_t* rmask = mask0 + k0 * a.allowed_row + (l >> 5);
+        uint32_t word[kRows];
+#pragma unroll
+        for (int g = 0; g < kRows; ++g) {
+          word[g] = 0u;
+          if (g < group) {
+            word[g] = *rmask;
+            rmask += a.allowed_row;
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < kRows; ++g) allowed |= ((word[g] >> (l & 31)) & 1u) << g;
+      } else {
+        allowed = ~0u;
+      }
+      if (draft)  // drafted before these rows
+        for (int64_t d = 0; d < k0; ++d) counted += draft[d] == (int64_t)token ? 1u : 0u;
+      T* rout = out0 + k0 * a.out_row + l;
+#pragma unroll
+      for (int g = 0; g < kRows; ++g) {
+        if (g >= group) break;
+        const uint32_t times = counted & ~kFlag;
+        if (drafted[g] == token) counted += 1u;  // from the next row on
+        if ((allowed >> g) & 1u) {
+          float f = to_f32(x[g]);
+          if ((counted & kFlag) || times) f = f > 0.0f ? __fdiv_rn(f, rho) : __fmul_rn(f, rho);
+          if (times) f = __fsub_rn(__fsub_rn(f, __fmul_rn(freq, (float)times)), pres);
+          if (id & kFlag) f = __fadd_rn(f, beta);
+          const T y = from_f32<T>(f);
+          *rout = y;
+          if (keyed) {
+            const unsigned long long own = a.greedy ? pack_key(to_f32(y), (uint32_t)token) : score(to_f32(y), k0 + g, l);
+            if (own > *reinterpret_cast<volatile unsigned long long*>(&listed_key[g])) atomicMax(&listed_key[g], own);
+          }
+        }
+        rout += a.out_row;
+      }
+    }
     __syncthreads();
     if (keyed && tid < group) {
       unsigned long long top = listed_key[tid];
@@ -645,6 +643,11 @@ __global__ void __launch_bounds__(kCopyThreads, 2) copy_kernel(ConstrainArgs a, 
 
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
+// Shared memory of list_kernel: two bits per id, counts, bias entries, the list.
+int64_t list_bytes(int64_t part, int64_t entries, bool narrow, bool has_bias) {
+  return part / 4 + part * (narrow ? 2 : 4) * (has_bias ? 2 : 1) + round_up(std::min(part, entries) * 2, 16);
+}
+
 // The plan goes by sizes alone, so that a caller can make the scratch anywhere.
 ConstrainPlan plan_constrain(const ConstrainArgs& a) {
   constexpr int64_t num_sms = 148;
@@ -654,29 +657,32 @@ ConstrainPlan plan_constrain(const ConstrainArgs& a) {
   p.narrow = tokens <= 0xffff && a.bias_count <= 0xfffe ? 1 : 0;
   const int64_t vocab = round_up(a.vocab, kBlock);
   if (tokens + a.bias_count > 0 || a.tokens) {
-    // Parts: as few as shared memory allows, since each reads the history, but
-    // as many as there are SMs.
-    const int64_t bits_per_id = (p.narrow ? 16 : 32) * (p.has_bias ? 2 : 1) + 2;
-    const int64_t most = std::min<int64_t>(kMaxPart, (int64_t)kListSmem * 8 / bits_per_id) / kBlock * kBlock;
-    int64_t parts = (vocab + most - 1) / most;
-    parts = std::max(parts, std::min(num_sms / a.batch, vocab / (2 * kBlock)));
+    // Parts: as few as shared memory allows where the history is long, since
+    // each reads all of it; as many CTAs as there are SMs, or four times that
+    // where the history is one read of each thread.
+    const int64_t entries = tokens + a.bias_count;
+    const auto bytes = [&](int64_t part) { return list_bytes(part, entries, p.narrow, p.has_bias); };
+    int64_t most = kMaxPart;
+    while (bytes(most) > kListSmem) most -= kBlock;
+    const int64_t ctas = num_sms * (tokens <= 4096 ? 4 : 1);
+    const int64_t parts = std::max((vocab + most - 1) / most, std::min(ctas / a.batch, vocab / (2 * kBlock)));
     p.part = (int)round_up((vocab + parts - 1) / parts, kBlock);
     p.parts = (int)((vocab + p.part - 1) / p.part);
     p.list_threads = (int)std::min<int64_t>(kListThreads, std::max<int64_t>(256, round_up(p.part / 32, 32)));
   }
-  // Stretches: two CTAs of 512 threads per SM, in whole waves, each with at
-  // least a few vectors per thread; smaller ones where rows are few.
-  const int64_t slots = 2 * num_sms;
-  int64_t stretch = kMaxStretch;
-  for (int64_t waves = 1; waves <= 8; ++waves) {
+  // Stretches: as many CTAs as run at once, and as few waves of them as the
+  // largest stretch allows.
+  const int64_t slots = kCopyCtas * num_sms;
+  int64_t stretch = vocab;
+  for (int64_t waves = 1; waves <= 64; ++waves) {
     const int64_t each = std::max<int64_t>(1, waves * slots / a.batch);  // stretches of a sequence
     stretch = round_up((vocab + each - 1) / each, kBlock);
-    if (stretch <= 16384) break;
+    if (stretch <= kMaxStretch) break;
   }
-  if (stretch > 16384) stretch = 16384;
+  stretch = std::min<int64_t>(stretch, kMaxStretch);
   p.stretch = (int)stretch;
   p.stretches = (int)((a.vocab + stretch - 1) / stretch);
-  p.copy_threads = (int)std::min<int64_t>(kCopyThreads, std::max<int64_t>(64, stretch / 16 / 32 * 32));
+  p.copy_threads = (int)std::min<int64_t>(kCopyThreads, std::max<int64_t>(64, stretch / 32 / 32 * 32));
 
   p.entries = std::min<int64_t>(p.part, tokens + a.bias_count);
   const int64_t lists = a.batch * p.parts;
@@ -697,7 +703,7 @@ ConstrainPlan plan_constrain(const ConstrainArgs& a) {
 
 template <typename C>
 cudaError_t launch_list(const ConstrainArgs& a, const ConstrainPlan& p, cudaStream_t s) {
-  const size_t bytes = (size_t)p.part / 8 * 2 + (size_t)p.part * sizeof(C) * (p.has_bias ? 2 : 1);
+  const size_t bytes = (size_t)list_bytes(p.part, p.entries, p.narrow, p.has_bias);
   if (bytes > 40 * 1024) {
     const cudaError_t e =
         cudaFuncSetAttribute(list_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, kListSmem);
