@@ -26,6 +26,7 @@
 //                copy (67 us for 32 x 8 rows of 151936 bf16).
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -46,6 +47,9 @@ constexpr int kCopyCtas = 4;       // per SM
 constexpr int kMaxStretch = 16384;
 constexpr int kInFlight = 4;       // vectors, or listed logits, under way per thread
 constexpr int kRows = 8;           // rows copied before their listed logits are worked out
+template <int N>
+using Int = std::integral_constant<int, N>;
+
 constexpr uint32_t kFlag = 0x80000000u;  // of an entry's id: biased; of its count: in the prompt
 
 // The sizes of both kernels and the places in the scratch, for one call.
@@ -380,7 +384,8 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) copy_kernel(Constrain
       asm volatile("prefetch.global.L2 [%0];" ::"l"(row + at));
   }
 
-  // What is listed in the stretch: a run of entries in each part that it meets.
+  // What is listed in the stretch: a run of entries in each of the one or two
+  // parts that it meets (a part is no smaller than a stretch).
   for (int i = tid; i < words; i += threads) touched[i] = 0u;
   const float rho = a.repetition ? a.repetition[b] : a.repetition_value;
   const float freq = a.frequency ? a.frequency[b] : a.frequency_value;
@@ -388,48 +393,36 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) copy_kernel(Constrain
   const int64_t* draft = a.draft ? a.draft + b * a.draft_stride + a.draft_first : nullptr;
   const int blocks = p.parts ? p.part / kBlock : 1, block0 = (int)(c0 / kBlock), block1 = (int)((c0 + n + kBlock - 1) / kBlock);
   const int part0 = block0 / blocks, part1 = p.parts ? (block1 - 1) / blocks + 1 : part0;
-  auto run = [&](int part, int64_t* from, int64_t* to) {
-    const int64_t which = b * p.parts + part;
-    const uint32_t* before = plane<uint32_t>(a, p.before) + which * (blocks + 1);
-    *from = which * p.entries + before[max(block0 - part * blocks, 0)];
-    *to = which * p.entries + before[min(block1 - part * blocks, blocks)];
-  };
   const uint32_t* ids = plane<uint32_t>(a, p.ids);
   const uint32_t* counts = plane<uint32_t>(a, p.counts);
   const float* biases = plane<float>(a, p.biases);
   __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the lists are there
-  // One entry after another over the runs; each thread keeps its first.
-  int entries = 0;
-  for (int part = part0; part < part1; ++part) {
-    int64_t from, to;
-    run(part, &from, &to);
-    entries += (int)(to - from);
-  }
-  auto entry_at = [&](int e, uint32_t* id, uint32_t* counted, float* beta) {
-    for (int part = part0;; ++part) {
-      int64_t from, to;
-      run(part, &from, &to);
-      if (e < (int)(to - from) || part == part1 - 1) {
-        *id = ids[from + e];
-        *counted = counts[from + e];
-        *beta = p.has_bias ? biases[from + e] : 0.0f;  // of no meaning where the id has no flag
-        return;
-      }
-      e -= (int)(to - from);
+  int64_t run_from[2] = {0, 0};
+  int run_length[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (part0 + i < part1) {
+      const int part = part0 + i;
+      const int64_t which = b * p.parts + part;
+      const uint32_t* before = plane<uint32_t>(a, p.before) + which * (blocks + 1);
+      const uint32_t from = before[max(block0 - part * blocks, 0)];
+      run_from[i] = which * p.entries + from;
+      run_length[i] = (int)(before[min(block1 - part * blocks, blocks)] - from);
     }
-  };
-  uint32_t my_id = 0u, my_count = 0u;
-  float my_beta = 0.0f;
-  if (tid < entries) entry_at(tid, &my_id, &my_count, &my_beta);
   if (keyed) {
-    for (int e = tid; e < entries; e += threads) {
-      uint32_t id = my_id, counted;
-      float beta;
-      if (e != tid) entry_at(e, &id, &counted, &beta);
-      const int l = (int)((id & ~kFlag) - (uint32_t)c0);
-      atomicOr(&touched[l >> 5], 1u << (l & 31));
-    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      for (int e0 = tid; e0 < run_length[i]; e0 += threads * kInFlight) {
+        uint32_t id[kInFlight];
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) id[u] = ids[run_from[i] + min(e0 + u * threads, run_length[i] - 1)];
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) {
+          const int l = (int)((id[u] & ~kFlag) - (uint32_t)c0);
+          atomicOr(&touched[l >> 5], 1u << (l & 31));
+        }
+      }
     __syncthreads();
   }
 
@@ -560,64 +553,85 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) copy_kernel(Constrain
     }
     if (keyed) __syncthreads();  // before listed logits change the vectors just looked at
 
-    // The listed logits of these rows, after the copies of them, a thread for
-    // each entry and all rows. What the copy left in place of a masked one
-    // stays; in place, an allowed one's input is what the copy wrote.
-    for (int e = tid; e < entries; e += threads) {
-      uint32_t id = my_id, counted = my_count;
-      float beta = my_beta;
-      if (e != tid) entry_at(e, &id, &counted, &beta);
-      const int token = (int)(id & ~kFlag), l = (int)((uint32_t)token - (uint32_t)c0);
-      T x[kRows];
-      uint32_t allowed = 0u;
-      const T* rin = in0 + k0 * a.in_row + l;
+    // The listed logits of these rows, after the copies of them: EN entries in
+    // flight per thread, RN of their rows. What the copy left in place of a
+    // masked one stays; in place, an allowed one's input is what the copy wrote.
+    auto settle = [&](auto entries_in_flight, auto rows_in_flight) {
+      constexpr int EN = decltype(entries_in_flight)::value, RN = decltype(rows_in_flight)::value;
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        const int length = i == 0 ? run_length[0] : run_length[1];
+        const int64_t from = i == 0 ? run_from[0] : run_from[1];
+        for (int e0 = tid; e0 < length; e0 += threads * EN) {
+          uint32_t id[EN], counted[EN], allowed[EN];
+          float beta[EN];
+          T x[EN][RN];
 #pragma unroll
-      for (int g = 0; g < kRows; ++g) {
-        x[g] = from_f32<T>(0.0f);
-        if (g < group) {
-          x[g] = *rin;
-          rin += a.in_row;
-        }
-      }
-      if (mask0) {
-        const uint32_t* rmask = mask0 + k0 * a.allowed_row + (l >> 5);
-        uint32_t word[kRows];
+          for (int u = 0; u < EN; ++u) {
+            const int64_t e = from + min(e0 + u * threads, length - 1);
+            id[u] = ids[e];
+            counted[u] = counts[e];
+            beta[u] = p.has_bias ? biases[e] : 0.0f;  // of no meaning where the id has no flag
+          }
+          for (int g0 = 0; g0 < group; g0 += RN) {
 #pragma unroll
-        for (int g = 0; g < kRows; ++g) {
-          word[g] = 0u;
-          if (g < group) {
-            word[g] = *rmask;
-            rmask += a.allowed_row;
+            for (int u = 0; u < EN; ++u) {
+              const int l = (int)((id[u] & ~kFlag) - (uint32_t)c0);
+              const T* rin = in0 + (k0 + g0) * a.in_row + l;
+              const uint32_t* rmask = mask0 + (k0 + g0) * a.allowed_row + (l >> 5);
+              uint32_t word[RN];
+#pragma unroll
+              for (int g = 0; g < RN; ++g) {
+                x[u][g] = from_f32<T>(0.0f);
+                word[g] = ~0u;
+                if (g0 + g < group) {
+                  x[u][g] = rin[g * a.in_row];
+                  if (mask0) word[g] = rmask[g * a.allowed_row];
+                }
+              }
+              allowed[u] = 0u;
+#pragma unroll
+              for (int g = 0; g < RN; ++g) allowed[u] |= ((word[g] >> (l & 31)) & 1u) << g;
+            }
+            if (draft && g0 == 0)  // drafted before these rows
+              for (int64_t d = 0; d < k0; ++d) {
+                const int64_t t = draft[d];
+#pragma unroll
+                for (int u = 0; u < EN; ++u) counted[u] += t == (int64_t)(id[u] & ~kFlag) ? 1u : 0u;
+              }
+#pragma unroll
+            for (int u = 0; u < EN; ++u) {
+              if (e0 + u * threads >= length) break;
+              const int token = (int)(id[u] & ~kFlag), l = (int)((uint32_t)token - (uint32_t)c0);
+              T* rout = out0 + (k0 + g0) * a.out_row + l;
+#pragma unroll
+              for (int g = 0; g < RN; ++g) {
+                if (g0 + g >= group) break;
+                const uint32_t times = counted[u] & ~kFlag;
+                if (drafted[g0 + g] == token) counted[u] += 1u;  // from the next row on
+                if (!((allowed[u] >> g) & 1u)) continue;
+                float f = to_f32(x[u][g]);
+                if ((counted[u] & kFlag) || times) f = f > 0.0f ? __fdiv_rn(f, rho) : __fmul_rn(f, rho);
+                if (times) f = __fsub_rn(__fsub_rn(f, __fmul_rn(freq, (float)times)), pres);
+                if (id[u] & kFlag) f = __fadd_rn(f, beta[u]);
+                const T y = from_f32<T>(f);
+                rout[g * a.out_row] = y;
+                if (keyed) {
+                  const unsigned long long own =
+                      a.greedy ? pack_key(to_f32(y), (uint32_t)token) : score(to_f32(y), k0 + g0 + g, l);
+                  if (own > *reinterpret_cast<volatile unsigned long long*>(&listed_key[g0 + g]))
+                    atomicMax(&listed_key[g0 + g], own);
+                }
+              }
+            }
           }
         }
-#pragma unroll
-        for (int g = 0; g < kRows; ++g) allowed |= ((word[g] >> (l & 31)) & 1u) << g;
-      } else {
-        allowed = ~0u;
       }
-      if (draft)  // drafted before these rows
-        for (int64_t d = 0; d < k0; ++d) counted += draft[d] == (int64_t)token ? 1u : 0u;
-      T* rout = out0 + k0 * a.out_row + l;
-#pragma unroll
-      for (int g = 0; g < kRows; ++g) {
-        if (g >= group) break;
-        const uint32_t times = counted & ~kFlag;
-        if (drafted[g] == token) counted += 1u;  // from the next row on
-        if ((allowed >> g) & 1u) {
-          float f = to_f32(x[g]);
-          if ((counted & kFlag) || times) f = f > 0.0f ? __fdiv_rn(f, rho) : __fmul_rn(f, rho);
-          if (times) f = __fsub_rn(__fsub_rn(f, __fmul_rn(freq, (float)times)), pres);
-          if (id & kFlag) f = __fadd_rn(f, beta);
-          const T y = from_f32<T>(f);
-          *rout = y;
-          if (keyed) {
-            const unsigned long long own = a.greedy ? pack_key(to_f32(y), (uint32_t)token) : score(to_f32(y), k0 + g, l);
-            if (own > *reinterpret_cast<volatile unsigned long long*>(&listed_key[g])) atomicMax(&listed_key[g], own);
-          }
-        }
-        rout += a.out_row;
-      }
-    }
+    };
+    if (group > 2)
+      settle(Int<1>{}, Int<kRows>{});
+    else
+      settle(Int<kInFlight>{}, Int<1>{});
     __syncthreads();
     if (keyed && tid < group) {
       unsigned long long top = listed_key[tid];
@@ -656,20 +670,6 @@ ConstrainPlan plan_constrain(const ConstrainArgs& a) {
   const int64_t tokens = (a.history ? a.history_cap : 0) + a.draft_most;
   p.narrow = tokens <= 0xffff && a.bias_count <= 0xfffe ? 1 : 0;
   const int64_t vocab = round_up(a.vocab, kBlock);
-  if (tokens + a.bias_count > 0 || a.tokens) {
-    // Parts: as few as shared memory allows where the history is long, since
-    // each reads all of it; as many CTAs as there are SMs, or four times that
-    // where the history is one read of each thread.
-    const int64_t entries = tokens + a.bias_count;
-    const auto bytes = [&](int64_t part) { return list_bytes(part, entries, p.narrow, p.has_bias); };
-    int64_t most = kMaxPart;
-    while (bytes(most) > kListSmem) most -= kBlock;
-    const int64_t ctas = num_sms * (tokens <= 4096 ? 4 : 1);
-    const int64_t parts = std::max((vocab + most - 1) / most, std::min(ctas / a.batch, vocab / (2 * kBlock)));
-    p.part = (int)round_up((vocab + parts - 1) / parts, kBlock);
-    p.parts = (int)((vocab + p.part - 1) / p.part);
-    p.list_threads = (int)std::min<int64_t>(kListThreads, std::max<int64_t>(256, round_up(p.part / 32, 32)));
-  }
   // Stretches: as many CTAs as run at once, and as few waves of them as the
   // largest stretch allows.
   const int64_t slots = kCopyCtas * num_sms;
@@ -684,6 +684,20 @@ ConstrainPlan plan_constrain(const ConstrainArgs& a) {
   p.stretches = (int)((a.vocab + stretch - 1) / stretch);
   p.copy_threads = (int)std::min<int64_t>(kCopyThreads, std::max<int64_t>(64, stretch / 32 / 32 * 32));
 
+  if (tokens + a.bias_count > 0 || a.tokens) {
+    // Parts: as few as shared memory allows where the history is long, since
+    // each reads all of it; as many CTAs as there are SMs, or four times that
+    // where the history is one read of each thread.
+    const int64_t entries = tokens + a.bias_count;
+    const auto bytes = [&](int64_t part) { return list_bytes(part, entries, p.narrow, p.has_bias); };
+    int64_t most = kMaxPart;
+    while (bytes(most) > kListSmem) most -= kBlock;
+    const int64_t ctas = num_sms * (tokens <= 4096 ? 4 : 1);
+    const int64_t parts = std::max((vocab + most - 1) / most, std::min(ctas / a.batch, vocab / (2 * kBlock)));
+    p.part = (int)std::max(round_up((vocab + parts - 1) / parts, kBlock), stretch);  // a stretch meets two parts at most
+    p.parts = (int)((vocab + p.part - 1) / p.part);
+    p.list_threads = (int)std::min<int64_t>(kListThreads, std::max<int64_t>(256, round_up(p.part / 32, 32)));
+  }
   p.entries = std::min<int64_t>(p.part, tokens + a.bias_count);
   const int64_t lists = a.batch * p.parts;
   int64_t at = round_up(a.tokens ? a.batch * a.block * 8 : 0, 16);
