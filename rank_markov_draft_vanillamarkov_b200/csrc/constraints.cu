@@ -43,7 +43,7 @@ constexpr int kMaxPart = kListThreads * kRounds * 32;  // 16-bit places in its l
 constexpr int kListSmem = 222 * 1024;
 constexpr int kAhead = 8;          // history ids in flight per thread
 constexpr int kCopyThreads = 256;
-constexpr int kCopyCtas = 4;       // per SM
+constexpr int kCopyCtas = 3;       // per SM
 constexpr int kMaxStretch = 16384;
 constexpr int kInFlight = 4;       // vectors, or listed logits, under way per thread
 constexpr int kRows = 8;           // rows copied before their listed logits are worked out
@@ -56,7 +56,8 @@ constexpr uint32_t kFlag = 0x80000000u;  // of an entry's id: biased; of its cou
 struct ConstrainPlan {
   int has_bias, narrow;
   int part, parts, list_threads;  // ids per CTA of list_kernel, per sequence; parts 0: nothing is listed
-  int stretch, stretches, copy_threads;
+  int stretch, stretches, copy_threads;  // ids per CTA of copy_kernel, per sequence and rows
+  int rows, groups;                      // rows per CTA of it
   int64_t entries;                // places for entries per part
   // Byte offsets in the scratch: [rows] keys and [batch] counters, both cleared
   // by list_kernel; per part, the number of entries before each block and in
@@ -365,7 +366,8 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) copy_kernel(Constrain
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = (int)blockDim.x;
   const int64_t b = blockIdx.x / p.stretches;
   const int stretch = (int)(blockIdx.x % p.stretches);
-  const int64_t c0 = (int64_t)stretch * p.stretch, rows = a.block;
+  const int64_t c0 = (int64_t)stretch * p.stretch;
+  const int rows = (int)a.block, k_begin = (int)blockIdx.y * p.rows, k_end = rows - k_begin > p.rows ? k_begin + p.rows : rows;
   const int n = (int)min((int64_t)p.stretch, a.vocab - c0);
   const int words = p.stretch / 32, mask_last = (n + 31) / 32 - 1;
   const bool keyed = a.tokens != nullptr;
@@ -378,8 +380,8 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) copy_kernel(Constrain
   T* const out0 = static_cast<T*>(a.out) + b * a.out_batch + c0;
   const uint32_t* const mask0 = a.allowed ? a.allowed + b * a.allowed_batch + (c0 >> 5) : nullptr;
   // The first rows come into L2 while the lists are made.
-  for (int64_t k = 0; k < min(rows, (int64_t)kRows); ++k) {
-    const char* row = reinterpret_cast<const char*>(in0 + k * a.in_row);
+  for (int k = k_begin; k < min(k_end, k_begin + kRows); ++k) {
+    const char* row = reinterpret_cast<const char*>(in0 + (int64_t)k * a.in_row);
     for (int at = tid * 128; at < n * (int)sizeof(T); at += threads * 128)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(row + at));
   }
@@ -426,8 +428,8 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) copy_kernel(Constrain
     __syncthreads();
   }
 
-  for (int64_t k0 = 0; k0 < rows; k0 += kRows) {
-    const int group = (int)min((int64_t)kRows, rows - k0);
+  for (int k0 = k_begin; k0 < k_end; k0 += kRows) {
+    const int group = min(kRows, k_end - k0);
     if (tid < kRows) {
       listed_key[tid] = 0ull;
       const int64_t id = draft && k0 + tid < rows - 1 ? draft[k0 + tid] : -1;
@@ -438,9 +440,9 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) copy_kernel(Constrain
     // vector; a single element has the complement of its id. A row of -inf
     // alone keeps the first threads' own ids, of which the lowest wins. Listed
     // logits stand aside as -inf.
-    const T* in = in0 + k0 * a.in_row;
-    T* out = out0 + k0 * a.out_row;
-    const uint32_t* mask = mask0 ? mask0 + k0 * a.allowed_row : nullptr;
+    const T* in = in0 + (int64_t)k0 * a.in_row;
+    T* out = out0 + (int64_t)k0 * a.out_row;
+    const uint32_t* mask = mask0 ? mask0 + (int64_t)k0 * a.allowed_row : nullptr;
     for (int r = 0; r < group; ++r) {
       float best = -INFINITY;
       int best_at = tid < n ? ~tid : kNone;
@@ -537,7 +539,7 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) copy_kernel(Constrain
         const float top = warp_best[row][w];
         int id = ~at;
         if (at >= 0) {
-          const uint4 vec = *reinterpret_cast<const uint4*>(out0 + (k0 + row) * a.out_row + at);
+          const uint4 vec = *reinterpret_cast<const uint4*>(out0 + (int64_t)(k0 + row) * a.out_row + at);
           const uint32_t aside = bits_at<ALIGNED>(touched, at, words - 1);
           int first = 0;
 #pragma unroll
@@ -577,8 +579,8 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) copy_kernel(Constrain
 #pragma unroll
             for (int u = 0; u < EN; ++u) {
               const int l = (int)((id[u] & ~kFlag) - (uint32_t)c0);
-              const T* rin = in0 + (k0 + g0) * a.in_row + l;
-              const uint32_t* rmask = mask0 + (k0 + g0) * a.allowed_row + (l >> 5);
+              const T* rin = in0 + (int64_t)(k0 + g0) * a.in_row + l;
+              const uint32_t* rmask = mask0 + (int64_t)(k0 + g0) * a.allowed_row + (l >> 5);
               uint32_t word[RN];
 #pragma unroll
               for (int g = 0; g < RN; ++g) {
@@ -594,7 +596,7 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) copy_kernel(Constrain
               for (int g = 0; g < RN; ++g) allowed[u] |= ((word[g] >> (l & 31)) & 1u) << g;
             }
             if (draft && g0 == 0)  // drafted before these rows
-              for (int64_t d = 0; d < k0; ++d) {
+              for (int d = 0; d < k0; ++d) {
                 const int64_t t = draft[d];
 #pragma unroll
                 for (int u = 0; u < EN; ++u) counted[u] += t == (int64_t)(id[u] & ~kFlag) ? 1u : 0u;
@@ -603,7 +605,7 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) copy_kernel(Constrain
             for (int u = 0; u < EN; ++u) {
               if (e0 + u * threads >= length) break;
               const int token = (int)(id[u] & ~kFlag), l = (int)((uint32_t)token - (uint32_t)c0);
-              T* rout = out0 + (k0 + g0) * a.out_row + l;
+              T* rout = out0 + (int64_t)(k0 + g0) * a.out_row + l;
 #pragma unroll
               for (int g = 0; g < RN; ++g) {
                 if (g0 + g >= group) break;
@@ -645,12 +647,12 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) copy_kernel(Constrain
     __syncthreads();
     if (tid == 0) {
       __threadfence();
-      last = atomicAdd(plane<uint32_t>(a, p.counters) + b, 1u) == (uint32_t)p.stretches - 1u;
+      last = atomicAdd(plane<uint32_t>(a, p.counters) + b, 1u) == (uint32_t)(p.stretches * p.groups) - 1u;
       __threadfence();
     }
     __syncthreads();
     if (last)
-      for (int64_t k = tid; k < rows; k += threads)
+      for (int k = tid; k < rows; k += threads)
         a.tokens[b * a.tokens_batch + k] = (int64_t)key_token(__ldcg(plane<unsigned long long>(a, 0) + b * rows + k));
   }
 }
@@ -671,11 +673,16 @@ ConstrainPlan plan_constrain(const ConstrainArgs& a) {
   p.narrow = tokens <= 0xffff && a.bias_count <= 0xfffe ? 1 : 0;
   const int64_t vocab = round_up(a.vocab, kBlock);
   // Stretches: as many CTAs as run at once, and as few waves of them as the
-  // largest stretch allows.
+  // largest stretch allows. Where there are few, rows go to different CTAs
+  // rather than one after another.
   const int64_t slots = kCopyCtas * num_sms;
+  int64_t rows = a.block;
+  while (rows > 1 && a.batch * ((a.block + rows - 1) / rows) * (vocab / 2048 + 1) <= slots) rows = (rows + 1) / 2;
+  p.rows = (int)std::min<int64_t>(rows, 0x7fffffff);
+  p.groups = (int)((a.block + rows - 1) / rows);
   int64_t stretch = vocab;
   for (int64_t waves = 1; waves <= 64; ++waves) {
-    const int64_t each = std::max<int64_t>(1, waves * slots / a.batch);  // stretches of a sequence
+    const int64_t each = std::max<int64_t>(1, waves * slots / (a.batch * p.groups));  // stretches of a sequence's rows
     stretch = round_up((vocab + each - 1) / each, kBlock);
     if (stretch <= kMaxStretch) break;
   }
@@ -737,7 +744,7 @@ cudaError_t launch_copy(const ConstrainArgs& a, const ConstrainPlan& p, cudaStre
   };
   const bool aligned = whole(a.in, a.in_batch, a.in_row) && whole(a.out, a.out_batch, a.out_row);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(a.batch * p.stretches));
+  cfg.gridDim = dim3((unsigned)(a.batch * p.stretches), (unsigned)p.groups);
   cfg.blockDim = dim3((unsigned)p.copy_threads);
   cfg.dynamicSmemBytes = (size_t)p.stretch / 8;
   cfg.stream = s;

@@ -384,6 +384,24 @@ def test_captured_calls_follow_the_buffers():
         b.check(out, tokens)
 
 
+def test_one_row_for_many_sequences():
+    """An input row shared by all sequences (stride 0), each with its own history; written out of place."""
+    case = Case(5, 0, 3001, 40, 2, torch.bfloat16, "rows", seed=60)
+    case.logits[:] = case.logits[:1]
+    x = case.logits[0].cuda().expand(5, 3001)
+    case.check(*process_logits(x, case.constraints(), **case.call_args()))
+    with pytest.raises(DSparkError):
+        process_logits(x, case.constraints(), out=x, **case.call_args())
+
+
+@pytest.mark.parametrize("batch,block,vocab", [(1, 40, 700), (2, 9, 5000), (70, 3, 1500), (1, 70, 20000)])
+def test_long_blocks_count_every_drafted_token(batch, block, vocab):
+    """Blocks past the rows that one CTA takes, with the same tokens drafted again and again."""
+    case = Case(batch, block, vocab, 5, 3, torch.float32, "rows", seed=block)
+    case.draft = np.random.default_rng(1).integers(0, 3, (batch, block))
+    case.check(*process_logits(case.device_logits(), case.constraints(), **case.call_args()))
+
+
 def test_empty_calls():
     n = launch_count()
     c = TokenConstraints(50)
