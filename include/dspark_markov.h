@@ -393,7 +393,8 @@ int dspark_markov_clip_plan(const void* const* grads, void* const* outs, const i
  * overlap take one each. The sum of squares is formed in 64 bits from groups of
  * a few 32-bit sums, in an order fixed by the plan, and holds for any finite
  * values. An infinite norm scales by 0 and a NaN norm by NaN, as the formula
- * says; max_norm is not negative and not NaN. pieces == 0 writes norm = 0.
+ * says, but an infinite max_norm scales by 1 whatever the norm; max_norm is not
+ * negative and not NaN. pieces == 0 writes norm = 0.
  */
 #define DSPARK_CLIP_MAX_PARTIALS 1024
 #define DSPARK_CLIP_SCRATCH_BYTES 8192

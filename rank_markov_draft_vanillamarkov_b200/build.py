@@ -15,7 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libdspark_markov.so")
 SOURCES = ["abi.cu", "generic.cu", "apply_tc.cu", "sample_tc.cu", "backward_tc.cu", "fused_tc.cu", "sample_rows_tc.cu", "apply_wide_tc.cu",
            "constraints.cu", "loss.cu", "clip.cu"]
-HEADERS = ["common.cuh", "ptx.cuh", "kernels.h"]
+HEADERS = ["common.cuh", "ptx.cuh", "cluster.cuh", "kernels.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

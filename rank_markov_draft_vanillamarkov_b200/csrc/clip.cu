@@ -8,14 +8,19 @@
 // each CTA its own pieces again, the last first, since they were read last.
 // Small plans run both passes in one cluster, with its barrier between them.
 //
+// Bound by memory: two readings and a writing of 132 MB (two fp32 [129280, 128])
+// take 68 us, 5.8 TB/s counted so; what the second reading finds in L2 (126 MB)
+// saves little of it, since the writing displaces it. A plan of one to sixteen
+// pieces takes 8 us, of which most is the launch; two launches took 20.
+//
 // Squares of four elements are summed in 32 bits and then in 64. A group whose
 // sum leaves the range in which that is exact to a few roundings (it overflows,
 // or an element that is not zero vanishes) is summed again in 64 bits.
 #include <cmath>
 
 #include "common.cuh"
+#include "cluster.cuh"
 #include "kernels.h"
-#include "ptx.cuh"
 
 namespace dspark {
 
@@ -148,6 +153,7 @@ __device__ __forceinline__ double sum_pieces(const ClipArgs& a) {
 }
 
 __device__ __forceinline__ float factor_of(double norm, float max_norm) {
+  if (isinf(max_norm)) return 1.0f;  // measured only, whatever the norm
   const double ratio = (double)max_norm / (norm + 1e-6);
   return ratio > 1.0 ? 1.0f : (float)ratio;  // NaN stays NaN
 }

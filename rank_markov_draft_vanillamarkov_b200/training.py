@@ -92,7 +92,7 @@ class GradientClipper:
     in device memory (a host-to-device copy: create it before a graph capture);
     ``clip`` reads what the tensors hold at each call. Calls of one object are
     ordered on one stream or by events, as anything that writes the same
-    tensors is.
+    tensors is; the object is kept until they have run.
     """
 
     def __init__(self, grads: Sequence[torch.Tensor], *, out: Optional[Sequence[torch.Tensor]] = None):
@@ -135,7 +135,8 @@ class GradientClipper:
     def clip(self, max_norm: float) -> torch.Tensor:
         """Scales by min(1, max_norm / (norm + 1e-6)) and returns the norm before
         it, an fp32 scalar on the device. ``max_norm`` inf only measures (and
-        copies to ``out``). An infinite norm scales by 0 and a NaN norm by NaN."""
+        copies to ``out``), whatever the norm; otherwise an infinite norm
+        scales by 0 and a NaN norm by NaN."""
         max_norm = float(max_norm)
         if math.isnan(max_norm) or max_norm < 0.0:
             raise ValueError("max_norm must not be negative or NaN")

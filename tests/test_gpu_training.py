@@ -354,6 +354,15 @@ def test_clip_limits_and_non_finite_norms():
     norm = clip_grad_norm([dev], math.inf)
     assert torch.equal(dev.cpu(), g) and abs(norm.item() - g.double().norm().item()) <= 1e-6 * norm.item()
     assert clip_grad_norm([dev], 0.0).item() > 0 and not dev.any()
+    for bad in (math.inf, math.nan):  # measured only, and copied, whatever the norm
+        for n in (3000, 700000):
+            dev = torch.ones(n, device="cuda")
+            dev[n // 2] = bad
+            out = torch.empty_like(dev)
+            norm = GradientClipper([dev], out=[out]).clip(math.inf)
+            assert not math.isfinite(norm.item())
+            # x * 1 is x; of a NaN the payload is free (a product's is CUDA's own NaN).
+            assert torch.allclose(out, dev, rtol=0.0, atol=0.0, equal_nan=True)
     for bad, after in ((float("inf"), 0.0), (float("nan"), float("nan"))):
         dev = g.cuda()
         dev[2999] = bad
