@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <limits>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -190,8 +191,14 @@ bool constraints_ok(const dspark_markov_constraints* c) {
   if (!c || c->history_cap < 0 || c->history_stride < 0 || c->bias_count < 0 || c->bias_stride < 0) return false;
   if (c->bias_count > 0 && (!c->bias_ids || !c->bias_values)) return false;
   if (c->bias_count > 0x7fffffffll) return false;
-  return true;
+  return aligned_to(c->history, 8) && aligned_to(c->history_lens, 8) && aligned_to(c->prompt_lens, 8) &&
+         aligned_to(c->bias_ids, 8) && aligned_to(c->repetition, 4) && aligned_to(c->frequency, 4) &&
+         aligned_to(c->presence, 4) && aligned_to(c->bias_values, 4);
 }
+
+// An infinite temperature as the largest number, which leaves the noise alone
+// all the same but keeps -inf (not allowed) below every other score.
+float finite_temperature(float t) { return std::min(t, std::numeric_limits<float>::max()); }
 
 // Sizes that ids, counts and offsets of the kernels hold.
 bool constrain_sizes_ok(int64_t batch, int64_t block, int64_t vocab, int64_t history_cap, int64_t bias_count,
@@ -588,7 +595,8 @@ int dspark_markov_process_logits(const void* logits, void* out, int64_t batch, i
   const int64_t n_in = extent(batch, block, vocab, in_batch_stride, in_row_stride);
   const int64_t n_out = extent(batch, block, vocab, out_batch_stride, out_row_stride);
   if (n_in < 0 || n_out < 0 || !disjoint_rows(batch, block, vocab, out_batch_stride, out_row_stride) ||
-      !aligned_to(logits, lsize) || !aligned_to(out, lsize) || !aligned_to(scratch, 16))
+      !aligned_to(logits, lsize) || !aligned_to(out, lsize) || !aligned_to(scratch, 16) || !aligned_to(allowed, 4) ||
+      !aligned_to(draft_tokens, 8) || !aligned_to(tokens, 8))
     return DSPARK_ERR_INVALID_ARG;
   if (tokens && batch > 1 && tokens_stride < block) return DSPARK_ERR_INVALID_ARG;
   if (draft_tokens && batch > 1 && draft_stride < draft_first + block - 1) return DSPARK_ERR_INVALID_ARG;
@@ -623,7 +631,7 @@ int dspark_markov_process_logits(const void* logits, void* out, int64_t batch, i
   a.tokens = tokens;
   a.tokens_batch = tokens_stride;
   a.greedy = !(temperature >= 1e-5f) ? 1 : 0;
-  a.temperature = temperature;
+  a.temperature = finite_temperature(temperature);
   a.seed = seed;
   a.status = d->status;
   if (!scratch && constrain_scratch_bytes(a) > 0) return DSPARK_ERR_INVALID_ARG;
@@ -646,7 +654,8 @@ int dspark_markov_sample_block_constrained(const void* base_logits, const int64_
     return DSPARK_ERR_INVALID_ARG;
   if (batch == 0 || proposal_len == 0) return DSPARK_OK;
   if (!base_logits || !first_prev_token_ids || !w1 || !w2 || !sampled_tokens || !corrected_logits || !scratch ||
-      !aligned_to(scratch, 16))
+      !aligned_to(scratch, 16) || !aligned_to(allowed, 4) || !aligned_to(first_prev_token_ids, 8) ||
+      !aligned_to(sampled_tokens, 8))
     return DSPARK_ERR_INVALID_ARG;
   if (!constrain_sizes_ok(batch, proposal_len, vocab, constraints->history_cap, constraints->bias_count, proposal_len))
     return DSPARK_ERR_UNSUPPORTED;
@@ -679,7 +688,7 @@ int dspark_markov_sample_block_constrained(const void* base_logits, const int64_
   c.scratch = scratch;
   c.tokens_batch = proposal_len;
   c.greedy = !(temperature >= 1e-5f) ? 1 : 0;
-  c.temperature = temperature;
+  c.temperature = finite_temperature(temperature);
   c.seed = seed;
   c.status = d->status;
   for (int64_t k = 0; k < proposal_len; ++k) {
@@ -716,7 +725,9 @@ int dspark_markov_block_cross_entropy(const void* logits, const int64_t* targets
   if (rows < 0 || vocab <= 0 || !dtype_ok(logits_dtype) || !loss) return DSPARK_ERR_INVALID_ARG;
   if (rows > 0 && (!logits || !targets || !row_losses)) return DSPARK_ERR_INVALID_ARG;
   const size_t lsize = logits_dtype == DSPARK_DTYPE_BF16 ? 2 : 4;
-  if (!aligned_to(logits, lsize) || !aligned_to(grad, lsize)) return DSPARK_ERR_INVALID_ARG;
+  if (!aligned_to(logits, lsize) || !aligned_to(grad, lsize) || !aligned_to(targets, 8) || !aligned_to(weights, 4) ||
+      !aligned_to(loss, 4) || !aligned_to(row_losses, 4))
+    return DSPARK_ERR_INVALID_ARG;
   if (rows > 0x7fffffffll || bounded(rows, vocab, 0, 1ll << 60) < 0) return DSPARK_ERR_UNSUPPORTED;
   if (grad && grad != logits) {
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(logits), g0 = reinterpret_cast<uintptr_t>(grad);
@@ -780,7 +791,8 @@ int dspark_markov_clip_grad_norm(const dspark_markov_clip_piece* plan, int64_t p
   t_last_algo = 0;
   t_last_variant = 0;
   static_assert(DSPARK_CLIP_MAX_PARTIALS * sizeof(double) <= DSPARK_CLIP_SCRATCH_BYTES, "partials fit the scratch");
-  if (pieces < 0 || !(max_norm >= 0.0f) || !norm || !scratch || !aligned_to(scratch, 8) || (pieces > 0 && !plan))
+  if (pieces < 0 || !(max_norm >= 0.0f) || !norm || !scratch || !aligned_to(scratch, 8) || !aligned_to(norm, 4) ||
+      !aligned_to(plan, 8) || (pieces > 0 && !plan))
     return DSPARK_ERR_INVALID_ARG;
   int err = DSPARK_OK;
   DeviceState* d = device_state(&err);

@@ -20,17 +20,22 @@
 //   copy_kernel  masks and copies the rows by 16-byte vectors, a stretch of
 //                the vocabulary of one sequence per CTA and up to eight rows
 //                at a time, then works out the listed logits of those rows,
-//                one thread for each. Within the copy they would cost every
-//                warp the whole arithmetic for a lane or two, and counting in
-//                each of the many CTAs that a copy needs cost more than the
-//                copy (67 us for 32 x 8 rows of 151936 bf16).
+//                one thread for each.
+//
+// Measured, 32 x 8 rows of 151936 bf16 logits behind 2048 tokens, masks, greedy:
+// 66 us (2.4 TB/s of 160 MB), of which the lists are about 11, the copy 26 to 33
+// and the listed logits the rest: scattered 2-byte reads and writes, about one
+// 32-byte sector each way per listed logit. Other divisions cost more: listed
+// logits within the copy 113 us (every warp runs the whole arithmetic for a lane
+// or two), a history counted by a cluster through each other's shared memory 91,
+// the listed logits in a third kernel 72, the state counted by every CTA of the
+// copy 67 (but 70 us rather than 57 for 64 rows behind 32768 tokens).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
-#include "ptx.cuh"
 
 namespace dspark {
 
@@ -43,7 +48,9 @@ constexpr int kMaxPart = kListThreads * kRounds * 32;  // 16-bit places in its l
 constexpr int kListSmem = 222 * 1024;
 constexpr int kAhead = 8;          // history ids in flight per thread
 constexpr int kCopyThreads = 256;
-constexpr int kCopyCtas = 3;       // per SM
+// Per SM: a copy of 32 x 8 x 151936 takes 66 us with three, of 80 registers a
+// thread, 71 with four, which leave it 64, and as much with two of 512 threads.
+constexpr int kCopyCtas = 3;
 constexpr int kMaxStretch = 16384;
 constexpr int kInFlight = 4;       // vectors, or listed logits, under way per thread
 constexpr int kRows = 8;           // rows copied before their listed logits are worked out
@@ -430,6 +437,7 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) copy_kernel(Constrain
 
   for (int k0 = k_begin; k0 < k_end; k0 += kRows) {
     const int group = min(kRows, k_end - k0);
+    if (k0 > k_begin) __syncthreads();  // the last rows' keys have been read
     if (tid < kRows) {
       listed_key[tid] = 0ull;
       const int64_t id = draft && k0 + tid < rows - 1 ? draft[k0 + tid] : -1;
@@ -674,7 +682,8 @@ ConstrainPlan plan_constrain(const ConstrainArgs& a) {
   const int64_t vocab = round_up(a.vocab, kBlock);
   // Stretches: as many CTAs as run at once, and as few waves of them as the
   // largest stretch allows. Where there are few, rows go to different CTAs
-  // rather than one after another.
+  // rather than one after another, each of which then reads the lists (7 x 5
+  // rows of 32003: 17 us, 30 with a sequence's rows in one CTA).
   const int64_t slots = kCopyCtas * num_sms;
   int64_t rows = a.block;
   while (rows > 1 && a.batch * ((a.block + rows - 1) / rows) * (vocab / 2048 + 1) <= slots) rows = (rows + 1) / 2;

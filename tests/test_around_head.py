@@ -150,7 +150,17 @@ def test_c_entry_refusals(lib):
     assert entropy(rows=-1) == bad and entropy(dt=7) == bad and entropy(row=None) == bad
     assert entropy(grad=ctypes.c_void_p((1 << 20) + 16)) == bad and entropy(grad=ctypes.c_void_p((1 << 40) + 2)) == bad
     assert entropy(rows=1 << 40) == N.DSPARK_ERR_UNSUPPORTED
+    # Addresses between elements.
+    odd = ctypes.c_void_p((1 << 20) + 2)
+    assert process(al=odd) == bad and process(draft=odd, tok=None) == bad and process(tok=odd, scratch=far) == bad
+    assert entropy(t=odd) == bad and entropy(loss=odd) == bad and entropy(row=odd) == bad
+    for field in ("history", "history_lens", "prompt_lens", "repetition", "frequency", "presence", "bias_ids",
+                  "bias_values"):
+        d = N.Constraints()
+        setattr(d, field, (1 << 20) + 2)
+        assert process(con=ctypes.byref(d)) == bad, field
     cl = lib.dspark_markov_clip_grad_norm
+    assert cl(ctypes.c_void_p(1028), 1, 1.0, p, p, None) == bad and cl(p, 1, 1.0, odd, p, None) == bad
     assert cl(None, 1, 1.0, p, p, None) == bad and cl(p, -1, 1.0, p, p, None) == bad
     assert cl(p, 1, -1.0, p, p, None) == bad and cl(p, 1, float("nan"), p, p, None) == bad
     assert cl(p, 1, 1.0, None, p, None) == bad and cl(p, 1, 1.0, p, None, None) == bad

@@ -402,6 +402,33 @@ def test_long_blocks_count_every_drafted_token(batch, block, vocab):
     case.check(*process_logits(case.device_logits(), case.constraints(), **case.call_args()))
 
 
+@pytest.mark.parametrize("temperature", [0.7, float("inf")])
+@pytest.mark.parametrize("batch,block,vocab,dtype", [(3, 40, 70, torch.float32), (1, 9, 33, torch.bfloat16),
+                                                     (300, 17, 600, torch.bfloat16), (2, 8, 30000, torch.float32)])
+def test_draws_of_a_block(batch, block, vocab, dtype, temperature):
+    """The C entry draws from the constrained logits of a block; only allowed tokens, at any temperature."""
+    case = Case(batch, block, vocab, 6, 3, dtype, "rows", seed=batch)
+    case.allowed[..., 5] = True
+    x, args, c = case.device_logits(), case.call_args(), case.constraints()
+    out, tokens = torch.empty_like(x), torch.empty(batch, block, dtype=torch.int64, device="cuda")
+    scratch = c._scratch(x.device, batch, block, block - 1, True)
+    words = args["allowed"].shape[-1]
+    for _ in range(5):
+        N.check(N.load().dspark_markov_process_logits(
+            x.data_ptr(), out.data_ptr(), batch, block, vocab, block * vocab, vocab, block * vocab, vocab, c._ref,
+            args["draft_tokens"].data_ptr(), block, 0, args["allowed"].data_ptr(), block * words, words,
+            tokens.data_ptr(), block, temperature, 77, scratch.data_ptr(), 0 if dtype == torch.float32 else 1,
+            torch.cuda.current_stream().cuda_stream), "process_logits")
+        got, picks = f64(out), tokens.cpu().numpy()
+        if _ == 0:
+            case.check(out, None)
+        for b in range(0, batch, max(1, batch // 8)):
+            for k in range(block):
+                assert case.allowed[b, k, picks[b, k]], (b, k)
+                s = got[b, k] / min(temperature, 1e38) + gumbel_noise(77, b, k, vocab)
+                assert s[picks[b, k]] >= s.max() - 1e-4, (b, k)
+
+
 def test_empty_calls():
     n = launch_count()
     c = TokenConstraints(50)
