@@ -247,8 +247,9 @@ __global__ void __launch_bounds__(kMaxThreads, 2) loss_rows_kernel(LossArgs a, L
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
     abort_flag = 0;
-    mbar_init(&met_bar[0], (uint32_t)(ranks * warps));
-    mbar_init(&met_bar[1], (uint32_t)(ranks * warps));
+    const uint32_t arrivals = ranks > 1 ? 1u : (uint32_t)warps;  // a cluster's pairs count as bytes
+    mbar_init(&met_bar[0], arrivals);
+    mbar_init(&met_bar[1], arrivals);
     fence_barrier_init();
   }
 
@@ -347,7 +348,9 @@ __global__ void __launch_bounds__(kMaxThreads, 2) loss_rows_kernel(LossArgs a, L
           }
         s = (part[0].x + part[0].y) + (part[1].x + part[1].y);
       }
-      float top = m;
+      // The target's logit changes no maximum; with it here, it has been read
+      // before the pair leaves, after which an in-place gradient may replace it.
+      float top = fmaxf(m, xt);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       s = rescaled(s, m, top);
@@ -356,14 +359,13 @@ __global__ void __launch_bounds__(kMaxThreads, 2) loss_rows_kernel(LossArgs a, L
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       // The warp's pair to every CTA. The other of the two buffers may still
       // be read; this one was left by all warps before they sent the pairs
-      // that ended the last row's wait. An arrival also says that the warp has
-      // read what it needs of the row outside its vectors.
-      __syncwarp();
+      // that ended the last row's wait. Stores that the barrier counts, since an
+      // arrival that releases one waits for the last row's gradients as well.
       if (ranks > 1) {
-        if (lane < ranks) {
-          store_remote(remote_u32(&pairs[parity][rank * warps + warp], (uint32_t)lane), m, s);
-          mbar_arrive_remote(remote_u32(&met_bar[parity], (uint32_t)lane));
-        }
+        if (tid == 0) mbar_arrive_expect_tx(&met_bar[parity], (uint32_t)(ranks * warps * sizeof(float2)));
+        if (lane < ranks)
+          store_async(remote_u32(&pairs[parity][rank * warps + warp], (uint32_t)lane), m, s,
+                      remote_u32(&met_bar[parity], (uint32_t)lane));
       } else if (lane == 0) {
         pairs[parity][warp] = make_float2(m, s);
         mbar_arrive(&met_bar[parity]);
