@@ -19,11 +19,12 @@
 // more here than bulk copies through shared memory, which held the same kernel
 // to 4.3 TB/s whatever it computed.
 //
-// Measured: 2560 rows of 129280 bf16, a fifth of them ignored, 256 us (4.7 TB/s
-// of 1.19 GB; a plain copy of as many bytes 190 us), 320 rows 47 us (3.5 TB/s;
-// the copy 33 us), 320 fp32 rows 76 us (4.4 TB/s; 57 us). What keeps it from the
+// Measured: 2560 rows of 129280 bf16, a fifth of them ignored, 248 us (4.8 TB/s
+// of 1.19 GB; a plain copy of as many bytes 190 us), 320 rows 46 us (3.6 TB/s;
+// the copy 33 us), 320 fp32 rows 70 us (4.8 TB/s; 57 us). What keeps it from the
 // copy: two exponentials a logit at 16 per clock and SM take 18 us for 320 rows,
-// and a call of few rows fills and empties the SMs once with little between.
+// and 71 clusters of four run at once, so that 320 rows go in five rounds of
+// which the last is half empty.
 #include <algorithm>
 #include <cmath>
 #include <mutex>
