@@ -445,16 +445,17 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) copy_kernel(Constrain
     }
 
     // The copy. Greedy keys: the largest value so far and the first id of its
-    // vector; a single element has the complement of its id. A row of -inf
-    // alone keeps the first threads' own ids, of which the lowest wins. Listed
-    // logits stand aside as -inf.
+    // vector; a single element has the complement of its id. Keys of both kinds
+    // begin with -inf at the first threads' own ids, so that a row of -inf alone
+    // takes the lowest, id 0, whichever of its logits are listed. Listed logits
+    // stand aside as -inf.
     const T* in = in0 + (int64_t)k0 * a.in_row;
     T* out = out0 + (int64_t)k0 * a.out_row;
     const uint32_t* mask = mask0 ? mask0 + (int64_t)k0 * a.allowed_row : nullptr;
     for (int r = 0; r < group; ++r) {
       float best = -INFINITY;
       int best_at = tid < n ? ~tid : kNone;
-      unsigned long long key = 0ull;
+      unsigned long long key = tid < n ? pack_key(-INFINITY, (uint32_t)(c0 + tid)) : 0ull;
       // Strictly larger, or the first NaN: ids rise, so equal values keep the lower one.
       auto better = [&](float y) { return y > best || (y != y && best == best); };
       auto single = [&](int l) {

@@ -429,6 +429,47 @@ def test_draws_of_a_block(batch, block, vocab, dtype, temperature):
                 assert s[picks[b, k]] >= s.max() - 1e-4, (b, k)
 
 
+def _draw(c, x, out, draft, allowed, temperature, seed=77):
+    """The tokens of a (B, M, V) view drawn by the C entry into the view ``out``."""
+    batch, block, vocab = x.shape
+    tokens = torch.full((batch, block), -5, dtype=torch.int64, device="cuda")
+    scratch = c._scratch(x.device, batch, block, block - 1 if draft is not None else 0, True)
+    words = allowed.shape[-1] if allowed is not None else 0
+    N.check(N.load().dspark_markov_process_logits(
+        x.data_ptr(), out.data_ptr(), batch, block, vocab, x.stride(0), x.stride(1), out.stride(0), out.stride(1),
+        c._ref, draft.data_ptr() if draft is not None else None, block, 0,
+        allowed.data_ptr() if allowed is not None else None, block * words, words, tokens.data_ptr(), block,
+        temperature, seed, scratch.data_ptr(), 0 if x.dtype == torch.float32 else 1,
+        torch.cuda.current_stream().cuda_stream), "process_logits")
+    return tokens
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("vocab", [1, 5, 13, 1001, 32003])
+@pytest.mark.parametrize("listed", ["all", "first", "last", "none"])
+def test_draws_of_rows_that_allow_nothing(listed, vocab, dtype):
+    """Token 0, wherever rows start in and out, whatever the history lists; other rows draw what they allow."""
+    ids = {"all": list(range(vocab)), "first": [0], "last": [vocab - 1], "none": []}[listed]
+    history = torch.tensor([ids, ids], dtype=torch.int64, device="cuda").view(2, len(ids))
+    c = TokenConstraints(vocab, history=history, repetition_penalty=1.2, presence_penalty=0.5)
+    masks = np.zeros((2, 3, vocab), dtype=bool)
+    masks[1, 1, vocab // 2] = True
+    allowed = _words(masks).cuda()
+    g = torch.Generator().manual_seed(vocab)
+    for at_in, at_out in ((0, 0), (1, 1), (0, 1), (1, 3), (5, 5)):
+        hold = torch.zeros(6 * vocab + 16, dtype=dtype, device="cuda")
+        x = hold[at_in: at_in + 6 * vocab].view(2, 3, vocab)
+        x.copy_(torch.randn(2, 3, vocab, generator=g))
+        other = torch.zeros(6 * vocab + 16, dtype=dtype, device="cuda")
+        out = other[at_out: at_out + 6 * vocab].view(2, 3, vocab)
+        for temperature in (0.7, 1e-3, float("inf"), 0.0):
+            want = [[0, 0, 0], [0, vocab // 2, 0]]
+            assert _draw(c, x, out, None, allowed, temperature).tolist() == want, (at_in, at_out, temperature)
+            assert bool((out[0] == float("-inf")).all())
+        assert _draw(c, x, x, None, allowed, 0.7).tolist() == want
+    assert device_status() == 0
+
+
 def test_empty_calls():
     n = launch_count()
     c = TokenConstraints(50)
@@ -528,6 +569,26 @@ def test_constrained_sampler(batch, m, vocab, rank, ldt, wdt, temperature):
             else:
                 s = a[i, k] / temperature + gumbel_noise(77, i, k, vocab)
                 assert s[picks[i, k]] >= s.max() - 1e-4, (i, k)
+    assert device_status() == 0
+
+
+@pytest.mark.parametrize("vocab,dtype", [(5, torch.bfloat16), (13, torch.bfloat16), (1001, torch.float32),
+                                         (2056, torch.bfloat16)])
+@pytest.mark.parametrize("temperature", [0.0, 0.8])
+def test_constrained_sampler_of_rows_that_allow_nothing(vocab, dtype, temperature):
+    """Such a position gives token 0, which the next position then follows like any other."""
+    head = _head(vocab, 64, dtype, seed=vocab)
+    base = torch.randn(3, 4, vocab, device="cuda").to(dtype)
+    history = torch.arange(vocab, device="cuda").expand(3, vocab).contiguous()
+    masks = np.zeros((3, 4, vocab), dtype=bool)
+    masks[1, 2, vocab - 2] = True
+    tokens, logits = head.sample_block_tokens(
+        base, first_prev_token_ids=torch.tensor([1, 2, 3], device="cuda"), temperature=temperature, seed=5,
+        constraints=TokenConstraints(vocab, history=history, frequency_penalty=0.5), allowed=_words(masks).cuda())
+    want = torch.zeros(3, 4, dtype=torch.int64)
+    want[1, 2] = vocab - 2
+    assert torch.equal(tokens.cpu(), want)
+    assert np.array_equal(f64(logits) > -np.inf, masks)
     assert device_status() == 0
 
 
