@@ -239,9 +239,11 @@ class VanillaMarkov:
         cross entropy against ``targets`` (..., M) (training.block_cross_entropy)
         and the gradients of W1 and W2 (into ``grad_w1`` and ``grad_w2`` if
         given), clipped to a norm of ``max_norm`` unless that is None.
-        ``clipper`` is a GradientClipper over the given gradient buffers and
-        whatever else is clipped with them, for steps that keep their buffers;
-        without one the two gradients are clipped by their own joint norm.
+        ``clipper`` is a GradientClipper over the given gradient buffers (each
+        one of its gradients or a part of one) and whatever else is clipped
+        with them, for steps that keep their buffers; the gradients returned
+        are then the clipped ones, in its ``out`` if it has one. Without a
+        clipper the two gradients are clipped by their own joint norm.
         Returns a dict: ``loss``, ``row_losses``, ``grad_logits`` (the gradient
         of the base logits, unclipped; it takes the corrected logits' buffer,
         ``corrected`` if given), ``grad_w1``, ``grad_w2`` and ``norm`` (None
@@ -251,13 +253,17 @@ class VanillaMarkov:
             raise ValueError("base_logits is empty")
         if clipper is not None and (grad_w1 is None or grad_w2 is None or max_norm is None):
             raise ValueError("clipper needs max_norm and the gradient buffers that it was made for")
+        clipped = (clipper.clipped(grad_w1), clipper.clipped(grad_w2)) if clipper is not None else None
         out = self.apply_block_logits(base_logits, token_ids=token_ids, out=corrected)
         loss, row_losses, grad = block_cross_entropy(out, targets, weights=weights, ignore_index=ignore_index,
                                                      reduction=reduction, out_grad=out)
         gw1, gw2 = self.apply_block_logits_backward(grad, token_ids=token_ids, grad_w1=grad_w1, grad_w2=grad_w2)
         norm = None
-        if max_norm is not None:
-            norm = clipper.clip(max_norm) if clipper is not None else clip_grad_norm([gw1, gw2], max_norm)
+        if clipper is not None:
+            norm = clipper.clip(max_norm)
+            gw1, gw2 = clipped
+        elif max_norm is not None:
+            norm = clip_grad_norm([gw1, gw2], max_norm)
         return {"loss": loss, "row_losses": row_losses, "grad_logits": grad, "grad_w1": gw1, "grad_w2": gw2,
                 "norm": norm}
 

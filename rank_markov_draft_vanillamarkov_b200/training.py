@@ -7,6 +7,7 @@ A step is ``apply_block_logits`` -> ``block_cross_entropy`` ->
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 import math
 from typing import Optional, Sequence, Tuple
@@ -110,6 +111,7 @@ class GradientClipper:
             if o is not g:
                 _check_cuda(o, f"out[{i}]", self.device)
         self.grads, self.outs = grads, outs
+        self._starts = sorted((g.data_ptr(), i) for i, g in enumerate(grads) if g.numel())
         lib = N.load()
         n = len(grads)
         args = ((ctypes.c_void_p * n)(*[g.data_ptr() for g in grads]), (ctypes.c_void_p * n)(*[o.data_ptr() for o in outs]),
@@ -130,6 +132,20 @@ class GradientClipper:
         if code == N.DSPARK_ERR_INVALID_ARG:
             raise ValueError("gradients and outputs must not overlap one another")
         N.check(code, "dspark_markov_clip_plan")
+
+    def clipped(self, grad: torch.Tensor) -> torch.Tensor:
+        """Where ``clip`` leaves ``grad``, which is one of ``grads`` or a contiguous
+        part of one: ``grad`` itself, or its place in ``out``."""
+        at, size = grad.data_ptr(), grad.element_size()
+        k = bisect.bisect_right(self._starts, (at, len(self.grads))) - 1
+        if k >= 0 and grad.is_contiguous() and grad.device == self.device:
+            start, i = self._starts[k]
+            g, o = self.grads[i], self.outs[i]
+            if g.dtype == grad.dtype and at + grad.numel() * size <= start + g.numel() * size:
+                if o.data_ptr() == start:
+                    return grad
+                return o.view(-1)[(at - start) // size:][: grad.numel()].view(grad.shape)
+        raise ValueError("not one of the clipper's gradients")
 
     @_ranged
     def clip(self, max_norm: float) -> torch.Tensor:

@@ -453,6 +453,49 @@ def test_teacher_forced_step(batch, blocks, vocab, rank, ldt, wdt):
         head.teacher_forced_gradients(base, token_ids=prev, targets=targets.cuda(), clipper=GradientClipper(bufs))
 
 
+def test_teacher_forced_step_returns_what_its_clipper_leaves():
+    """The clipped gradients come back wherever the clipper writes them; a clipper of other buffers is refused."""
+    vocab, rank = 515, 16
+    g = torch.Generator().manual_seed(1)
+    head = VanillaMarkov(*((torch.randn(vocab, rank, generator=g) * 0.3).cuda() for _ in range(2)))
+    base = torch.randn(2, 3, vocab, generator=g).cuda()
+    ids = dict(token_ids=torch.randint(0, vocab, (2, 3), generator=g).cuda(),
+               targets=torch.randint(0, vocab, (2, 3), generator=g).cuda())
+    raw = head.teacher_forced_gradients(base, **ids)
+    n = vocab * rank
+    norm = math.sqrt(sum((f64(raw[k]) ** 2).sum() for k in ("grad_w1", "grad_w2")))
+
+    def check(step, extra=0.0):
+        total = math.sqrt(norm ** 2 + extra)
+        assert abs(step["norm"].item() - total) <= around.CLIP_NORM_REL * total
+        for k in ("grad_w1", "grad_w2"):
+            exact = f64(raw[k]) * (norm / 8 / (total + 1e-6))
+            _within(f64(step[k]), exact, (around.CLIP_NORM_REL + 4 * around.U32) * np.abs(exact) + 2.0 ** -133)
+
+    bufs, outs = ([torch.empty(vocab, rank, device="cuda") for _ in range(2)] for _ in range(2))
+    flat, flat_out = (torch.zeros(2 * n + 11, device="cuda") for _ in range(2))
+    flat[0] = 3.0
+    parts, part_outs = ([f[11 + i * n: 11 + (i + 1) * n].view(vocab, rank) for i in range(2)] for f in (flat, flat_out))
+    tail = torch.ones(7, dtype=torch.bfloat16, device="cuda")
+    for given, clipper, at, extra in (
+            (bufs, GradientClipper(bufs), bufs, 0.0),
+            (bufs, GradientClipper(bufs, out=outs), outs, 0.0),
+            (bufs, GradientClipper([tail, bufs[1], bufs[0]], out=[torch.empty_like(tail), outs[1], outs[0]]), outs, 7.0),
+            (parts, GradientClipper([flat], out=[flat_out]), part_outs, 9.0),
+            (parts, GradientClipper([flat]), parts, 9.0)):
+        step = head.teacher_forced_gradients(base, grad_w1=given[0], grad_w2=given[1], max_norm=norm / 8,
+                                             clipper=clipper, **ids)
+        check(step, extra)
+        for k, want in zip(("grad_w1", "grad_w2"), at):
+            assert step[k].data_ptr() == want.data_ptr() and step[k].shape == want.shape
+    keep = [b.clone() for b in bufs]
+    for wrong in (GradientClipper(outs), GradientClipper([bufs[0], outs[1]]), GradientClipper([]),
+                  GradientClipper([bufs[0], bufs[1][:-1]])):
+        with pytest.raises(ValueError):
+            head.teacher_forced_gradients(base, grad_w1=bufs[0], grad_w2=bufs[1], max_norm=1.0, clipper=wrong, **ids)
+    assert all(torch.equal(a, b) for a, b in zip(keep, bufs))  # refused before any work
+
+
 def test_training_and_constrained_serving_together():
     """A step's update changes the head; the updated head then drafts under constraints that it obeys."""
     g = torch.Generator().manual_seed(0)
