@@ -379,9 +379,15 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) copy_kernel(Constrain
   const int words = p.stretch / 32, mask_last = (n + 31) / 32 - 1;
   const bool keyed = a.tokens != nullptr;
   constexpr int kNone = 0x7fffffff;
+  // The key of a draw. A quotient from 2^127 on, in whose place 2^127 + |y| / 4
+  // stands, keeps the order of the logits and is finite where the logit is: a
+  // logit near the lowest value ranks above -inf (not allowed) at any
+  // temperature. No noise reaches that far.
   auto score = [&](float y, int64_t k, int l) {
     const uint32_t v = (uint32_t)(c0 + l);
-    return pack_key(y / a.temperature + noise_for(a.seed, (uint32_t)b, (uint32_t)(a.draft_first + k), v), v);
+    float q = y / a.temperature;
+    if (fabsf(q) >= 0x1p127f && !isinf(y)) q = copysignf(0x1p127f, y) + 0.25f * y;
+    return pack_key(q + noise_for(a.seed, (uint32_t)b, (uint32_t)(a.draft_first + k), v), v);
   };
   const T* const in0 = static_cast<const T*>(a.in) + b * a.in_batch + c0;
   T* const out0 = static_cast<T*>(a.out) + b * a.out_batch + c0;

@@ -470,6 +470,39 @@ def test_draws_of_rows_that_allow_nothing(listed, vocab, dtype):
     assert device_status() == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("temperature", [1e-5, 0.1, 0.7, 1.0, 3.0])
+@pytest.mark.parametrize("listed", [False, True], ids=["copied", "listed"])
+def test_draws_from_logits_whose_quotient_leaves_the_range(listed, temperature, dtype):
+    """Only allowed tokens, and of those the largest where they lie further apart than any noise."""
+    vocab, low = 700, torch.finfo(dtype).min
+    at = [699, 400, 130, 33, 3]
+    # Allowed logits of each row, by those ids; the largest, or None where several are.
+    rows = [([low] * 5, None), ([low, low, -1e38, low, low], 130), ([-1e38, low, -3e38, low, -2e38], 699),
+            ([1e38, 3e38, 2e38, 1.0, low], 400), ([3e38, -low, 3.2e38, 0.0, 0.0], 400), ([-2e37, -1e37, low, low, low], 400),
+            ([float("-inf"), low, float("-inf"), low, low], None), ([float("inf"), -low, 0.0, 1.0, 2.0], 699)]
+    x = torch.zeros(len(rows), 1, vocab)
+    masks = np.zeros((len(rows), 1, vocab), dtype=bool)
+    masks[:, 0, at] = True
+    for i, (values, _) in enumerate(rows):
+        x[i, 0, at] = torch.tensor(values)
+    x = x.to(dtype).cuda()
+    # Penalties that change nothing keep listed logits as they are.
+    c = TokenConstraints(vocab, history=torch.tensor(at, device="cuda").expand(len(rows), 5).contiguous()) if listed \
+        else TokenConstraints(vocab)
+    finite = [np.isfinite(f64(x[i, 0, at])) for i in range(len(rows))]
+    for seed in range(20):
+        out = torch.empty_like(x)
+        picks = _draw(c, x, out, None, _words(masks).cuda(), temperature, seed)[:, 0].tolist()
+        assert torch.equal(_bits(out[:, :, at]), _bits(x[:, :, at]))
+        for i, (_, want) in enumerate(rows):
+            if want is not None:
+                assert picks[i] == want, (i, seed)
+            else:
+                assert picks[i] in at and finite[i][at.index(picks[i])], (i, seed)
+    assert device_status() == 0
+
+
 def test_empty_calls():
     n = launch_count()
     c = TokenConstraints(50)
