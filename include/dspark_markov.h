@@ -352,7 +352,9 @@ int dspark_markov_sample_block_constrained(const void* base_logits, const int64_
  *
  * Sums are fp32 or wider and in a fixed order; the gradient is rounded once. A
  * live row that holds NaN or +inf, or -inf everywhere, has a NaN loss and
- * gradient. rows == 0 writes loss = 0.
+ * gradient. rows == 0 writes loss = 0. Where a wait between CTAs runs out
+ * (DSPARK_STATUS_TIMEOUT), the rows that it leaves undone have a NaN loss, and
+ * so has their sum.
  */
 int dspark_markov_block_cross_entropy(const void* logits, const int64_t* targets, const float* weights, int64_t rows,
                                       int64_t vocab, int64_t ignore_index, int32_t mean, float* loss,

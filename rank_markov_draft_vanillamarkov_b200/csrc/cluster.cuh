@@ -21,6 +21,10 @@ __device__ __forceinline__ uint32_t remote_u32(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
   return r;
 }
+// The minimum into another CTA's shared variable (an address of remote_u32).
+__device__ __forceinline__ void cluster_min(uint32_t addr, int x) {
+  asm volatile("red.relaxed.cluster.shared::cluster.min.s32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
 // Eight bytes into the shared memory of a CTA of this cluster, counted by a
 // barrier of that CTA as they land. Only in launches with a cluster.
 __device__ __forceinline__ void store_async(uint32_t addr, float a, float b, uint32_t bar) {

@@ -43,6 +43,8 @@ constexpr int kSumThreads = 512;  // of the kernels of one CTA per row or per ca
 constexpr int kMaxCluster = 16;
 constexpr int kWholeCtas = 8;     // of a launch that is one cluster
 constexpr int kMaxVectors = 16;   // of a row, in a thread's registers
+constexpr int kNoFailure = 0x7fffffff;
+constexpr uint64_t kDrainNs = 2000000000ull;  // the least limit of a wait for copies under way
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
 
@@ -228,6 +230,43 @@ __device__ __forceinline__ int slice_vectors(const LossPlan& p, int vecs, int ra
   return max(0, min(p.slice, vecs - rank * p.slice));
 }
 
+// A wait that expired ends its warp's rows. In all CTAs of the cluster the other
+// warps' waits expire then too, at most one row later, since a row's wait needs
+// the pairs of every warp. So each warp has sent its pair `failed`, counted from
+// zero, and some have sent the next one. Those that have not send it now, so
+// that both barriers complete and no CTA leaves before all stores to its shared
+// memory have landed. The losses from the failed row on are NaN; gradients that
+// are not written stay as they were.
+__device__ void end_failed_rows(const LossArgs& a, int ranks, int failed, int sent, uint64_t* met_bar, float2* pairs) {
+  const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = (int)blockDim.x >> 5;
+  const int rank = ranks > 1 ? (int)cluster_rank() : 0;
+  if (ranks > 1) {
+    const int next = failed + 1;
+    if (sent == next) {
+      float2* slots = pairs + (next & 1) * (kMaxCluster * kMaxWarps);
+      if (tid == 0) mbar_arrive_expect_tx(&met_bar[next & 1], (uint32_t)(ranks * warps * sizeof(float2)));
+      if (lane < ranks)
+        store_async(remote_u32(&slots[rank * warps + warp], (uint32_t)lane), 0.0f, 0.0f,
+                    remote_u32(&met_bar[next & 1], (uint32_t)lane));
+    }
+    if (tid == 0) {
+      volatile int never = 0;
+      const WaitCtl ctl{&never, a.status, a.wait_limit_ns > kDrainNs ? a.wait_limit_ns : kDrainNs};
+      for (int k = failed; k <= next; ++k) mbar_wait_cluster(&met_bar[k & 1], (uint32_t)(k >> 1) & 1u, ctl);
+    }
+  }
+  if (rank == 0 && tid == 0) {
+    int before = 0;
+    for (int64_t i = blockIdx.x / ranks; i < a.rows; i += gridDim.x / ranks) {
+      int64_t t;
+      float w;
+      const bool live = live_row(a, i, &t, &w);
+      if (before >= failed) a.row_losses[i] = live ? NAN : 0.0f;
+      if (live) ++before;
+    }
+  }
+}
+
 // SAME: the gradient's rows start at the same offset from a 16-byte address as
 // the logits' (in place, or any vocabulary of whole vectors), so that a vector
 // read is a vector written; otherwise gradients are written one by one.
@@ -237,7 +276,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) loss_rows_kernel(LossArgs a, L
   __shared__ uint64_t met_bar[2];  // a row's pairs are here
   __shared__ float2 pairs[2][kMaxCluster * kMaxWarps];
   __shared__ double sums[kMaxWarps];
-  __shared__ int abort_flag;
+  __shared__ int abort_flag, first_failed;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = (int)threadIdx.x;
   const int threads = (int)blockDim.x, warps = threads >> 5;
   const int ranks = p.cluster, rank = ranks > 1 ? (int)cluster_rank() : 0;
@@ -248,6 +287,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) loss_rows_kernel(LossArgs a, L
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
     abort_flag = 0;
+    first_failed = kNoFailure;
     const uint32_t arrivals = ranks > 1 ? 1u : (uint32_t)warps;  // a cluster's pairs count as bytes
     mbar_init(&met_bar[0], arrivals);
     mbar_init(&met_bar[1], arrivals);
@@ -299,8 +339,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) loss_rows_kernel(LossArgs a, L
   __syncthreads();
   if (ranks > 1) cluster_barrier();  // every CTA's barriers are there
 
-  int parity = 0;
-  uint32_t met_phase = 0;
+  int sent = 0;  // pairs of this warp: live rows so far
   while (i < rows) {
     const int next = rows - i > step ? i + step : rows;
     int next_t = 0;
@@ -362,6 +401,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) loss_rows_kernel(LossArgs a, L
       // be read; this one was left by all warps before they sent the pairs
       // that ended the last row's wait. Stores that the barrier counts, since an
       // arrival that releases one waits for the last row's gradients as well.
+      const int parity = sent & 1;
       if (ranks > 1) {
         if (tid == 0) mbar_arrive_expect_tx(&met_bar[parity], (uint32_t)(ranks * warps * sizeof(float2)));
         if (lane < ranks)
@@ -371,6 +411,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) loss_rows_kernel(LossArgs a, L
         pairs[parity][warp] = make_float2(m, s);
         mbar_arrive(&met_bar[parity]);
       }
+      ++sent;
       __syncwarp();
       const float row_xt = xt, row_edge = edge;
       if (next_live) load_singles(next, next_shape, next_t);
@@ -378,7 +419,14 @@ __global__ void __launch_bounds__(kMaxThreads, 2) loss_rows_kernel(LossArgs a, L
       const int at = t - shape.head, vec = at >= 0 ? at / kE - rank * p.slice : -1;
       const bool own_target = vec >= 0 && vec < count && vec / (32 * NV) == warp && vec % 32 == lane;
       const float scale = (float)((double)w * inv_n);
-      mbar_wait_cluster(&met_bar[parity], met_phase, ctl);
+      if (!__all_sync(0xffffffffu, mbar_wait_cluster(&met_bar[parity], ((uint32_t)(sent - 1) >> 1) & 1u, ctl))) {
+        if (ranks > 1) {
+          if (lane < ranks) cluster_min(remote_u32(&first_failed, (uint32_t)lane), sent - 1);
+        } else if (lane == 0) {
+          atomicMin(&first_failed, sent - 1);
+        }
+        break;
+      }
       // Each warp for itself. Without NaN, which is orderable above all: a
       // warp's maximum is NaN only where it has no number at all.
       const int met = ranks * warps;
@@ -396,8 +444,6 @@ __global__ void __launch_bounds__(kMaxThreads, 2) loss_rows_kernel(LossArgs a, L
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      parity ^= 1;
-      if (parity == 0) met_phase ^= 1u;
       if (isinf(m)) s = NAN;  // +inf somewhere, or -inf everywhere
       const float factor = scale / s, unit = unit_for(m), ref = reference(m);
       if (rank == 0 && tid == 0)  // in plain units where the exponents' would overflow
@@ -440,7 +486,11 @@ __global__ void __launch_bounds__(kMaxThreads, 2) loss_rows_kernel(LossArgs a, L
     live = next_live;
   }
   __syncwarp();
-  if (ranks > 1) cluster_barrier();  // no CTA leaves while others may still send to it
+  if (ranks > 1)
+    cluster_barrier();  // no CTA leaves while others may still send to it
+  else
+    __syncthreads();
+  if (first_failed != kNoFailure) end_failed_rows(a, ranks, first_failed, sent, met_bar, &pairs[0][0]);
   if (p.whole) {
     cluster_barrier();  // every row's loss is written
     if (blockIdx.x == 0) sum_loss(a, sums);

@@ -9,7 +9,8 @@ import torch
 import oracle
 from oracle import around
 from rank_markov_draft_vanillamarkov_b200 import (DSparkError, GradientClipper, TokenConstraints, VanillaMarkov,
-                                                  block_cross_entropy, clip_grad_norm, device_status, set_algo)
+                                                  block_cross_entropy, clip_grad_norm, device_status, set_algo,
+                                                  set_debug)
 from rank_markov_draft_vanillamarkov_b200 import _native as N
 from rank_markov_draft_vanillamarkov_b200.build import build
 
@@ -241,6 +242,35 @@ def test_loss_long_offsets():
     loss, row, grad = block_cross_entropy(x, t, out_grad=x)
     _check_loss((loss, row[at], grad[at.cuda()]), pick, tp, None)
     assert not grad[1: rows - 2].any()
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("rows,vocab", [(10, 1024), (300, 8000), (700, 33), (90, 33001), (2000, 151936), (64, 300000)])
+def test_loss_waits_that_expire(rows, vocab, dtype):
+    """With a limit that any wait may pass, a row either has its loss and gradient or a NaN loss that the status word
+    reports, and the call after it is right. Nothing is withheld: every wait would be met a little later."""
+    g = torch.Generator("cuda").manual_seed(rows)
+    x = (torch.randn(rows, vocab, generator=g, device="cuda") * 3).to(dtype)
+    t = torch.randint(0, vocab, (rows,), generator=g, device="cuda")
+    t[::7] = -100
+    want = block_cross_entropy(x, t)
+    assert device_status() == 0
+    set_debug(0, 1)
+    try:
+        for place in ("out", "in place") * 3:
+            logits = x.clone()
+            loss, row, grad = block_cross_entropy(logits, t, out_grad=logits if place == "in place" else None)
+            status = device_status()
+            lost = row.isnan()
+            assert status == (N.DSPARK_STATUS_TIMEOUT if lost.any() else 0)
+            assert bool(loss.isnan()) == bool(lost.any()) and not lost[t == -100].any()
+            assert torch.equal(row[~lost], want[1][~lost])
+            kept = ~lost & (t != -100)
+            assert torch.equal(_bits(grad[kept]), _bits(want[2][kept]))
+    finally:
+        set_debug(0, 0)
+    again = block_cross_entropy(x, t)
+    assert all(torch.equal(a, b) for a, b in zip(again, want)) and device_status() == 0
 
 
 def test_loss_refusals():
