@@ -99,7 +99,7 @@ __device__ __forceinline__ double piece_squares(const T* g, int n) {
     uint4 raw[kInFlight];
 #pragma unroll
     for (int u = 0; u < kInFlight; ++u)
-      raw[u] = j + u * kThreads < vecs ? __ldg(from + j + u * kThreads) : make_uint4(0u, 0u, 0u, 0u);
+      raw[u] = j + u * kThreads < vecs ? from[j + u * kThreads] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
     for (int u = 0; u < kInFlight; ++u) s += Piece<T>::squares(raw[u]);
   }

@@ -166,6 +166,13 @@ def test_c_entry_refusals(lib):
     assert cl(p, 1, 1.0, None, p, None) == bad and cl(p, 1, 1.0, p, None, None) == bad
 
 
+@pytest.mark.parametrize("source", ["constraints.cu", "loss.cu", "clip.cu"])
+def test_no_read_only_loads_of_what_a_kernel_may_write(source):
+    """These kernels run in place; a read-only load asks for memory that the whole launch leaves alone."""
+    text = open(f"{B.CSRC}/{source}").read()
+    assert not any(form in text for form in ("__ldg", "ld.global.nc", "__restrict__"))
+
+
 def test_structs_match_the_header():
     # The library asserts the same sizes when it is compiled: eight 8-byte fields, three floats and their padding,
     # four 8-byte fields; two pointers and two 4-byte fields.
