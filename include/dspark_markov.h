@@ -400,7 +400,7 @@ int dspark_markov_clip_plan(const void* const* grads, void* const* outs, const i
  */
 #define DSPARK_CLIP_MAX_PARTIALS 1024
 #define DSPARK_CLIP_SCRATCH_BYTES 8192
-int dspark_markov_clip_grad_norm(const dspark_markov_clip_piece* plan, int64_t pieces, float max_norm, float* norm,
+int dspark_markov_clip_grad_norm(const dspark_markov_clip_piece* plan, int64_t pieces, double max_norm, float* norm,
                                  void* scratch, void* stream);
 
 /*

@@ -79,7 +79,7 @@ SIGNATURES = {
     "dspark_markov_block_cross_entropy": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _vp,
                                                          _i32, _vp]),
     "dspark_markov_clip_plan": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _vp, _i64, ctypes.POINTER(_i64)]),
-    "dspark_markov_clip_grad_norm": (ctypes.c_int, [_vp, _i64, _f32, _vp, _vp, _vp]),
+    "dspark_markov_clip_grad_norm": (ctypes.c_int, [_vp, _i64, ctypes.c_double, _vp, _vp, _vp]),
     "dspark_markov_get_status": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_int32)]),
     "dspark_markov_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "dspark_markov_set_algo": (_i32, [_i32]),

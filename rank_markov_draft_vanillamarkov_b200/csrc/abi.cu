@@ -786,12 +786,12 @@ int dspark_markov_clip_plan(const void* const* grads, void* const* outs, const i
   return DSPARK_OK;
 }
 
-int dspark_markov_clip_grad_norm(const dspark_markov_clip_piece* plan, int64_t pieces, float max_norm, float* norm,
+int dspark_markov_clip_grad_norm(const dspark_markov_clip_piece* plan, int64_t pieces, double max_norm, float* norm,
                                  void* scratch, void* stream) {
   t_last_algo = 0;
   t_last_variant = 0;
   static_assert(DSPARK_CLIP_MAX_PARTIALS * sizeof(double) <= DSPARK_CLIP_SCRATCH_BYTES, "partials fit the scratch");
-  if (pieces < 0 || !(max_norm >= 0.0f) || !norm || !scratch || !aligned_to(scratch, 8) || !aligned_to(norm, 4) ||
+  if (pieces < 0 || !(max_norm >= 0.0) || !norm || !scratch || !aligned_to(scratch, 8) || !aligned_to(norm, 4) ||
       !aligned_to(plan, 8) || (pieces > 0 && !plan))
     return DSPARK_ERR_INVALID_ARG;
   int err = DSPARK_OK;

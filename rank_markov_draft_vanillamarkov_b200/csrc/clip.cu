@@ -152,9 +152,9 @@ __device__ __forceinline__ double sum_pieces(const ClipArgs& a) {
   return s;
 }
 
-__device__ __forceinline__ float factor_of(double norm, float max_norm) {
+__device__ __forceinline__ float factor_of(double norm, double max_norm) {
   if (isinf(max_norm)) return 1.0f;  // measured only, whatever the norm
-  const double ratio = (double)max_norm / (norm + 1e-6);
+  const double ratio = max_norm / (norm + 1e-6);
   return ratio > 1.0 ? 1.0f : (float)ratio;  // NaN stays NaN
 }
 

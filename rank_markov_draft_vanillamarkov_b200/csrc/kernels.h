@@ -203,7 +203,7 @@ constexpr int64_t kClipPieceBytes = 65536;
 struct ClipArgs {
   const dspark_markov_clip_piece* plan;  // device memory
   int64_t pieces;
-  float max_norm;
+  double max_norm;
   float* norm;       // one element
   double* partials;  // DSPARK_CLIP_MAX_PARTIALS elements
 };

@@ -404,6 +404,24 @@ def test_clip_limits_and_non_finite_norms():
         assert math.isnan(out[2999].item())
 
 
+@pytest.mark.parametrize("n", [3000, 700000])
+def test_clip_limits_outside_fp32(n):
+    """A limit is a 64-bit number: a finite one above fp32's range still clips."""
+    g = torch.full((n,), 3e38)
+    g[::3] *= -0.5
+    for max_norm in (1e39, 5e40, 1e300):
+        dev = g.cuda()
+        out = torch.empty_like(dev)
+        norm = GradientClipper([dev], out=[out]).clip(max_norm)
+        assert norm.item() == math.inf  # as fp32
+        exact = f64(g) * around.clip([f64(g)], max_norm)[1]
+        _within(f64(out), exact, (around.CLIP_NORM_REL + 4 * around.U32) * np.abs(exact))
+    dev = g.cuda()
+    dev[1] = math.inf
+    assert clip_grad_norm([dev], 1e39).item() == math.inf
+    assert bool((dev[2:] == 0).all()) and math.isnan(dev[1].item())  # an infinite norm scales by zero
+
+
 def test_clip_repeats_streams_and_graphs():
     grads = _grads([(300001, F), (70000, B), (11, F)], seed=8)
     dev = [g.cuda() for g in grads]
