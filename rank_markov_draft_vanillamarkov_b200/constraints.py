@@ -84,7 +84,7 @@ class TokenConstraints:
                 self._take(x, f"{name}_penalty", x.shape[0])
                 setattr(c, name, x.data_ptr())
             else:
-                x = float(x)
+                x = ctypes.c_float(float(x)).value  # as the kernel gets it
                 if not math.isfinite(x) or (name == "repetition" and x <= 0.0):
                     raise ValueError(f"{name}_penalty must be finite" + (" and positive" if name == "repetition" else ""))
                 setattr(c, name + "_value", x)

@@ -199,6 +199,15 @@ def test_python_refusals_without_a_gpu():
         clip_grad_norm([torch.zeros(3)], 1.0)
 
 
+@pytest.mark.parametrize("penalty", [dict(frequency_penalty=1e39), dict(presence_penalty=-1e39),
+                                     dict(repetition_penalty=1e39), dict(repetition_penalty=1e-46)])
+def test_penalties_that_fp32_does_not_hold_are_refused(penalty):
+    """Finite numbers that would reach the kernel as an infinity or, for the repetition penalty, as zero."""
+    with pytest.raises(ValueError):
+        TokenConstraints(10, **penalty)
+    TokenConstraints(10, frequency_penalty=3e38, presence_penalty=1e-46, repetition_penalty=1e-40)
+
+
 @pytest.mark.parametrize("fn,name", [(C.process_logits, "process_logits"), (T.block_cross_entropy, "block_cross_entropy"),
                                      (T.GradientClipper.clip, "clip"),
                                      (VanillaMarkov.teacher_forced_gradients, "teacher_forced_gradients")])
