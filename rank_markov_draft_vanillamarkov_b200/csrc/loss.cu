@@ -446,10 +446,14 @@ __global__ void __launch_bounds__(kMaxThreads, 2) loss_rows_kernel(LossArgs a, L
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       if (isinf(m)) s = NAN;  // +inf somewhere, or -inf everywhere
       const float factor = scale / s, unit = unit_for(m), ref = reference(m);
-      if (rank == 0 && tid == 0)  // in plain units where the exponents' would overflow
-        a.row_losses[i] = unit == kLog2e && fabsf(row_xt) <= 0x1p126f
-                              ? kLn2 * (log2f(s) - fmaf(row_xt, unit, -ref))
-                              : logf(s) + (m - row_xt);
+      if (rank == 0 && tid == 0) {
+        // In plain units where the exponents' would overflow. Both terms lie
+        // around a rounded reference: where they cancel, what their rounding
+        // leaves below zero is zero (NaN stays).
+        const float nll = unit == kLog2e && fabsf(row_xt) <= 0x1p126f ? kLn2 * (log2f(s) - fmaf(row_xt, unit, -ref))
+                                                                      : logf(s) + (m - row_xt);
+        a.row_losses[i] = nll <= 0.0f ? 0.0f : nll;
+      }
       // The gradient at the target, which its owner writes over the rest.
       const float at_target = ex2(fmaf(row_xt, unit, -ref)) * factor - scale;
       if (g && rank == 0 && tid < shape.edges) {

@@ -245,6 +245,21 @@ def test_loss_long_offsets():
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("rows,vocab", [(40, 1024), (64, 20001), (4, 600001)])
+def test_losses_of_certain_rows_are_not_negative(rows, vocab, dtype):
+    """Rows whose target stands alone at the top, at references that round either way: a loss is never below zero."""
+    g = np.random.default_rng(rows)
+    for top in (1.0, 7.0, 25.0, 300.0, 3e4):
+        x = torch.from_numpy(g.normal(0, 0.1, (rows, vocab)) - 40.0).to(dtype)
+        t = torch.from_numpy(g.integers(0, vocab, rows))
+        x[torch.arange(rows), t] = torch.from_numpy(top * g.uniform(0.5, 1.0, rows)).to(dtype)
+        got = block_cross_entropy(x.cuda(), t.cuda())
+        assert not (got[1] < 0).any() and not got[0] < 0 and not torch.signbit(got[1]).any()
+        _check_loss(got, x, t, None)
+
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
 @pytest.mark.parametrize("rows,vocab", [(10, 1024), (300, 8000), (700, 33), (90, 33001), (2000, 151936), (64, 300000)])
 def test_loss_waits_that_expire(rows, vocab, dtype):
     """With a limit that any wait may pass, a row either has its loss and gradient or a NaN loss that the status word
