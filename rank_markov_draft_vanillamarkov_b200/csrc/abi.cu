@@ -653,12 +653,12 @@ int dspark_markov_sample_block_constrained(const void* base_logits, const int64_
       allowed_batch_stride < 0 || allowed_row_stride < 0)
     return DSPARK_ERR_INVALID_ARG;
   if (batch == 0 || proposal_len == 0) return DSPARK_OK;
+  if (!constrain_sizes_ok(batch, proposal_len, vocab, constraints->history_cap, constraints->bias_count, proposal_len))
+    return DSPARK_ERR_UNSUPPORTED;
   if (!base_logits || !first_prev_token_ids || !w1 || !w2 || !sampled_tokens || !corrected_logits || !scratch ||
       !aligned_to(scratch, 16) || !aligned_to(allowed, 4) || !aligned_to(first_prev_token_ids, 8) ||
       !aligned_to(sampled_tokens, 8))
     return DSPARK_ERR_INVALID_ARG;
-  if (!constrain_sizes_ok(batch, proposal_len, vocab, constraints->history_cap, constraints->bias_count, proposal_len))
-    return DSPARK_ERR_UNSUPPORTED;
   const size_t lsize = logits_dtype == DSPARK_DTYPE_BF16 ? 2 : 4;
   const int64_t n = extent(batch, proposal_len, vocab, proposal_len * vocab, vocab);
   const uintptr_t a0 = reinterpret_cast<uintptr_t>(base_logits), c0 = reinterpret_cast<uintptr_t>(corrected_logits);

@@ -371,8 +371,9 @@ class VanillaMarkov:
             code = self._lib.dspark_markov_sample_block_constrained(
                 base_logits.data_ptr(), prev.data_ptr(), batch, m, vocab, self.markov_w1.data_ptr(),
                 self.markov_w2.data_ptr(), self.markov_rank, temperature, seed & 0xFFFFFFFFFFFFFFFF, constraints._ref,
-                mask, mask_batch, mask_row, tokens.data_ptr(), corrected.data_ptr(), scratch.data_ptr(),
-                _DT[base_logits.dtype], _DT[self.weight_dtype], _stream_ptr(self.device))
+                mask, mask_batch, mask_row, tokens.data_ptr(), corrected.data_ptr(),
+                scratch.data_ptr() if scratch is not None else None, _DT[base_logits.dtype], _DT[self.weight_dtype],
+                _stream_ptr(self.device))
         N.check(code, "dspark_markov_sample_block_constrained")
         return tokens, corrected
 

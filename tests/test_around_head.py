@@ -173,6 +173,16 @@ def test_no_read_only_loads_of_what_a_kernel_may_write(source):
     assert not any(form in text for form in ("__ldg", "ld.global.nc", "__restrict__"))
 
 
+def test_constrained_sampler_refuses_sizes_before_it_asks_for_scratch(lib):
+    """Such sizes may have no scratch size, so that a caller has none to give."""
+    p, c = ctypes.c_void_p(1 << 20), N.Constraints()  # never dereferenced
+    for batch, m, vocab, cap in ((1 << 20, 1 << 20, 64, 0), (2, 3, 1 << 31, 0), (1, 1, 64, 1 << 30)):
+        c.history_cap = cap
+        assert lib.dspark_markov_sample_block_constrained(
+            p, p, batch, m, vocab, p, p, 16, 0.0, 0, ctypes.byref(c), None, 0, 0, p, ctypes.c_void_p(1 << 60), None, 0,
+            0, None) == N.DSPARK_ERR_UNSUPPORTED
+
+
 def test_structs_match_the_header():
     # The library asserts the same sizes when it is compiled: eight 8-byte fields, three floats and their padding,
     # four 8-byte fields; two pointers and two 4-byte fields.

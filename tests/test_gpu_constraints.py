@@ -664,3 +664,15 @@ def test_constrained_sampler_refusals():
                                  out_tokens=torch.zeros(2, 3, dtype=torch.int32, device="cuda"))
     with pytest.raises(DSparkError):
         head.sample_block_tokens(base, first_prev_token_ids=first, constraints=TokenConstraints(256), out_logits=base)
+
+
+def test_histories_past_the_supported_length_are_refused():
+    """By the library's error, from both callers; 8 GB that nothing touches."""
+    history = torch.empty(1, 1 << 30, dtype=torch.int64, device="cuda")
+    c = TokenConstraints(256, history=history, history_lens=torch.zeros(1, dtype=torch.int64, device="cuda"))
+    base = torch.zeros(1, 3, 256, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(DSparkError):
+        process_logits(base, c)
+    with pytest.raises(DSparkError):
+        _head(256, 64, torch.bfloat16, seed=4).sample_block_tokens(
+            base, first_prev_token_ids=torch.zeros(1, dtype=torch.int64, device="cuda"), constraints=c)
