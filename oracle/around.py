@@ -100,13 +100,13 @@ def cross_entropy(logits, targets, weights, ignore_index, mean, out_dtype):
         one = np.zeros(vocab)
         one[t] = 1.0
         grad[i] = w[i] * inv * (p - one)
-        # exp's own error, the rounding of its argument (|d| u, as an absolute error of the exponent) and one
-        # rescaling of a partial sum by another such exp, weighted as the terms are; then the sum's additions:
-        # at most `vocab` one after another.
+        # exp's own error and the rounding of its argument (|d| u, as an absolute error of the exponent), doubled for
+        # the rescaling of a partial sum by another such exp; weighted as the terms are. Then the sum's additions: at
+        # most `vocab` one after another.
         fin = np.where(np.isfinite(d), d, 0.0)
         rel = 2 * (EXP_ULPS + (EXP_ULPS_PER_X + 1) * np.abs(fin)) * 2 * U32
         depth = min(vocab, 1024) * U32
-        rel_s = float((p * rel).sum()) + rel[e > 0].max() * U32 + depth
+        rel_s = float((p * rel).sum()) + depth
         row_err[i] = rel_s + 4 * U32 * (abs(np.log(s)) + abs(fin[t]) + 1.0)
         if not np.isfinite(d[t]):
             row_err[i] = 0.0
@@ -130,6 +130,7 @@ def clip(grads, max_norm):
     return norm, min(1.0, max_norm / (norm + 1e-6))
 
 
-# The clipper forms squares and their sums in 32 bits within groups of at most 32 elements: 33 roundings, halved by
-# the root, and one rounding of the root itself.
-CLIP_NORM_REL = 33 * U32 / 2 + U32
+# The clipper forms squares of four elements and their sum in 32 bits, three roundings one after another at most (a
+# square, the multiply-add of another one, the sum of two such), halved by the root; the root is rounded once. The rest
+# is 64-bit: up to 2^17 additions in a row of 2^-53 each, halved too.
+CLIP_NORM_REL = 3 * U32 / 2 + U32 + 2.0 ** -37

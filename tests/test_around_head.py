@@ -54,6 +54,22 @@ def test_cross_entropy_by_hand_and_differences():
             assert abs((up - dn) / (2 * h) - grad[i, v]) <= 1e-8
 
 
+def test_clip_norm_bound_tells_groups_of_four_from_longer_sums():
+    """The bound holds for norms whose squares are summed by four in 32 bits, and not for 32 in a row."""
+    g = np.random.default_rng(0)
+    a, b, c, d = (g.uniform(1, 2, 20000).astype(np.float32) for _ in range(4))
+    fma = lambda x, z: (x.astype(np.float64) ** 2 + z).astype(np.float32)  # noqa: E731  x x is exact in 64 bits
+    four = (fma(a, b * b) + fma(c, d * d)).astype(np.float64)
+    exact = sum(x.astype(np.float64) ** 2 for x in (a, b, c, d))
+    norm = np.sqrt(four).astype(np.float32).astype(np.float64)
+    assert np.abs(norm / np.sqrt(exact) - 1).max() <= around.CLIP_NORM_REL
+    long = np.zeros_like(a)
+    for _ in range(32):
+        long = long + a * a
+    norm = np.sqrt(long.astype(np.float64))
+    assert np.abs(norm / np.sqrt(32 * a.astype(np.float64) ** 2) - 1).max() > around.CLIP_NORM_REL
+
+
 def _plan(lib, spans, capacity=None):
     n = len(spans)
     pieces = ctypes.c_int64(-1)
