@@ -307,13 +307,6 @@ struct Vec<float> {
   static __device__ __forceinline__ float get(const uint4& r, int e) {
     return __uint_as_float(e == 0 ? r.x : e == 1 ? r.y : e == 2 ? r.z : r.w);
   }
-  static __device__ __forceinline__ void set(uint4& r, int e, float x) {
-    const uint32_t b = __float_as_uint(x);
-    if (e == 0) r.x = b;
-    if (e == 1) r.y = b;
-    if (e == 2) r.z = b;
-    if (e == 3) r.w = b;
-  }
   // The largest element; NaN if there is one.
   static __device__ __forceinline__ float max_of(const uint4& r) {
     float m = get(r, 0);
@@ -339,14 +332,6 @@ struct Vec<__nv_bfloat16> {
   static __device__ __forceinline__ float get(const uint4& r, int e) {
     const uint32_t w = (e >> 1) == 0 ? r.x : (e >> 1) == 1 ? r.y : (e >> 1) == 2 ? r.z : r.w;
     return __uint_as_float((e & 1) ? (w & 0xffff0000u) : (w << 16));
-  }
-  static __device__ __forceinline__ void set(uint4& r, int e, float x) {
-    const uint32_t b = __bfloat16_as_ushort(__float2bfloat16_rn(x));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t& w = i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w;
-      if ((e >> 1) == i) w = (e & 1) ? (w & 0xffffu) | (b << 16) : (w & 0xffff0000u) | b;
-    }
   }
   static __device__ __forceinline__ float max_of(const uint4& r) {
     const auto p = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
