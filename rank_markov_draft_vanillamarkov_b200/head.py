@@ -135,10 +135,11 @@ class VanillaMarkov:
                 raise ValueError("out must match base_logits in shape and dtype")
             _check_cuda(out, "out", self.device)
         rows = base_logits.numel() // vocab
-        code = self._lib.dspark_markov_apply_block_logits(
-            base_logits.data_ptr(), out.data_ptr(), ids.data_ptr(), rows, vocab, self.markov_w1.data_ptr(),
-            self.markov_w2.data_ptr(), self.markov_rank, _DT[base_logits.dtype], _DT[self.weight_dtype],
-            _stream_ptr(self.device))
+        with _device_guard(self.device):
+            code = self._lib.dspark_markov_apply_block_logits(
+                base_logits.data_ptr(), out.data_ptr(), ids.data_ptr(), rows, vocab, self.markov_w1.data_ptr(),
+                self.markov_w2.data_ptr(), self.markov_rank, _DT[base_logits.dtype], _DT[self.weight_dtype],
+                _stream_ptr(self.device))
         N.check(code, "dspark_markov_apply_block_logits")
         return out
 
@@ -176,10 +177,11 @@ class VanillaMarkov:
         rows = hidden_states.numel() // d
         if rows == 0:
             return out
-        code = self._lib.dspark_markov_fused_lm_head_logits(
-            hidden_states.data_ptr(), ids.data_ptr(), rows, d, self.vocab_size, lm_head_weight.data_ptr(),
-            self.markov_w1.data_ptr(), self.markov_w2.data_ptr(), self.markov_rank, out.data_ptr(), _DT[out_dtype],
-            _DT[self.weight_dtype], _stream_ptr(self.device))
+        with _device_guard(self.device):
+            code = self._lib.dspark_markov_fused_lm_head_logits(
+                hidden_states.data_ptr(), ids.data_ptr(), rows, d, self.vocab_size, lm_head_weight.data_ptr(),
+                self.markov_w1.data_ptr(), self.markov_w2.data_ptr(), self.markov_rank, out.data_ptr(), _DT[out_dtype],
+                _DT[self.weight_dtype], _stream_ptr(self.device))
         N.check(code, "dspark_markov_fused_lm_head_logits")
         return out
 
@@ -220,11 +222,12 @@ class VanillaMarkov:
                 raise ValueError(f"{name} must be fp32 (V, r)")
             _check_cuda(buf, name, self.device)
             outs.append(buf)
-        code = self._lib.dspark_markov_apply_block_logits_backward(
-            g.data_ptr(), ids.data_ptr(), ids.numel(), vocab, self.markov_w1.data_ptr(), self.markov_w2.data_ptr(),
-            rank, outs[0].data_ptr() if outs[0] is not None else None,
-            outs[1].data_ptr() if outs[1] is not None else None, 1 if accumulate else 0, _DT[g.dtype],
-            _DT[self.weight_dtype], _stream_ptr(self.device))
+        with _device_guard(self.device):
+            code = self._lib.dspark_markov_apply_block_logits_backward(
+                g.data_ptr(), ids.data_ptr(), ids.numel(), vocab, self.markov_w1.data_ptr(), self.markov_w2.data_ptr(),
+                rank, outs[0].data_ptr() if outs[0] is not None else None,
+                outs[1].data_ptr() if outs[1] is not None else None, 1 if accumulate else 0, _DT[g.dtype],
+                _DT[self.weight_dtype], _stream_ptr(self.device))
         N.check(code, "dspark_markov_apply_block_logits_backward")
         return outs[0], outs[1]
 
@@ -295,10 +298,11 @@ class VanillaMarkov:
         rows = ids.numel()
         if rows == 0:
             return out, emb
-        code = self._lib.dspark_markov_transition_logits(
-            ids.data_ptr(), rows, self.vocab_size, self.markov_w1.data_ptr(), self.markov_w2.data_ptr(),
-            self.markov_rank, out.data_ptr(), emb.data_ptr() if emb is not None else None, _DT[wdt],
-            _stream_ptr(self.device))
+        with _device_guard(self.device):
+            code = self._lib.dspark_markov_transition_logits(
+                ids.data_ptr(), rows, self.vocab_size, self.markov_w1.data_ptr(), self.markov_w2.data_ptr(),
+                self.markov_rank, out.data_ptr(), emb.data_ptr() if emb is not None else None, _DT[wdt],
+                _stream_ptr(self.device))
         N.check(code, "dspark_markov_transition_logits")
         return out, emb
 
@@ -345,10 +349,11 @@ class VanillaMarkov:
         corrected = out_logits if out_logits is not None else torch.empty_like(base_logits)
         if constraints is not None or allowed is not None:
             return self._sample_constrained(base_logits, prev, t, seed, tokens, corrected, constraints, allowed)
-        code = self._lib.dspark_markov_sample_block(
-            base_logits.data_ptr(), prev.data_ptr(), batch, m, vocab, self.markov_w1.data_ptr(),
-            self.markov_w2.data_ptr(), self.markov_rank, t, seed & 0xFFFFFFFFFFFFFFFF, tokens.data_ptr(),
-            corrected.data_ptr(), _DT[base_logits.dtype], _DT[self.weight_dtype], _stream_ptr(self.device))
+        with _device_guard(self.device):
+            code = self._lib.dspark_markov_sample_block(
+                base_logits.data_ptr(), prev.data_ptr(), batch, m, vocab, self.markov_w1.data_ptr(),
+                self.markov_w2.data_ptr(), self.markov_rank, t, seed & 0xFFFFFFFFFFFFFFFF, tokens.data_ptr(),
+                corrected.data_ptr(), _DT[base_logits.dtype], _DT[self.weight_dtype], _stream_ptr(self.device))
         N.check(code, "dspark_markov_sample_block")
         return tokens, corrected
 
@@ -410,10 +415,11 @@ class VanillaMarkov:
         t = 0.0 if temperature is None else float(temperature)
         if math.isnan(t):
             raise ValueError("temperature is NaN")
-        code = self._lib.dspark_markov_sample_block_noalloc(
-            base_logits.data_ptr(), prev.data_ptr(), batch, m, vocab, self.markov_w1.data_ptr(),
-            self.markov_w2.data_ptr(), self.markov_rank, t, seed & 0xFFFFFFFFFFFFFFFF, out_tokens.data_ptr(),
-            out_logits.data_ptr(), _DT[base_logits.dtype], _DT[self.weight_dtype], _stream_ptr(self.device))
+        with _device_guard(self.device):
+            code = self._lib.dspark_markov_sample_block_noalloc(
+                base_logits.data_ptr(), prev.data_ptr(), batch, m, vocab, self.markov_w1.data_ptr(),
+                self.markov_w2.data_ptr(), self.markov_rank, t, seed & 0xFFFFFFFFFFFFFFFF, out_tokens.data_ptr(),
+                out_logits.data_ptr(), _DT[base_logits.dtype], _DT[self.weight_dtype], _stream_ptr(self.device))
         N.check(code, "dspark_markov_sample_block_noalloc")
 
 

@@ -239,3 +239,44 @@ def test_penalties_that_fp32_does_not_hold_are_refused(penalty):
                                      (VanillaMarkov.teacher_forced_gradients, "teacher_forced_gradients")])
 def test_entry_points_are_ranged(fn, name):
     assert fn.__wrapped__.__name__ == name
+
+
+def test_the_heads_calls_are_made_on_its_device(monkeypatch):
+    """The library launches on the current device, which may be another one: every call into it, those of a
+    teacher-forced step among them, stands inside the guard that makes the head's device the current one."""
+    from rank_markov_draft_vanillamarkov_b200 import head as H
+    inside, calls = [], []
+
+    class Guard:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            inside.append(self.device)
+
+        def __exit__(self, *exc):
+            inside.pop()
+
+    class Library:
+        def __getattr__(self, name):
+            def call(*args):
+                calls.append((name, list(inside)))
+                return N.DSPARK_OK
+            return call
+
+    for module in (H, T, C):
+        monkeypatch.setattr(module, "_device_guard", Guard)
+        monkeypatch.setattr(module, "_check_cuda", lambda *a: None)
+        monkeypatch.setattr(module, "_stream_ptr", lambda device: 0)
+    monkeypatch.setattr(N, "load", Library)
+    w = torch.zeros(64, 16)
+    head = VanillaMarkov(w, w)
+    x, ids = torch.zeros(2, 3, 64), torch.zeros(2, 3, dtype=torch.int64)
+    head.apply_block_logits(x, token_ids=ids)
+    head.apply_block_logits_backward(x, token_ids=ids)
+    head.transition_logits(ids)
+    head.fused_lm_head_logits(torch.zeros(2, 3, 8), torch.zeros(64, 8), token_ids=ids)
+    head.sample_block_tokens(x, first_prev_token_ids=ids[:, 0])
+    head.sample_block_tokens_noalloc(x, first_prev_token_ids=ids[:, 0].contiguous(), out_tokens=ids, out_logits=x)
+    head.teacher_forced_gradients(x, token_ids=ids, targets=ids)
+    assert len(calls) == 9 and all(at == [head.device] for _, at in calls), calls
