@@ -246,7 +246,10 @@ class VanillaMarkov:
         one of its gradients or a part of one) and whatever else is clipped
         with them, for steps that keep their buffers; the gradients returned
         are then the clipped ones, in its ``out`` if it has one. Without a
-        clipper the two gradients are clipped by their own joint norm.
+        clipper the two gradients are clipped by their own joint norm through
+        ``clip_grad_norm``, which stops the host until they are there and
+        cannot be captured into a graph. One process; see the module of
+        GradientClipper for several ranks.
         Returns a dict: ``loss``, ``row_losses``, ``grad_logits`` (the gradient
         of the base logits, unclipped; it takes the corrected logits' buffer,
         ``corrected`` if given), ``grad_w1``, ``grad_w2`` and ``norm`` (None

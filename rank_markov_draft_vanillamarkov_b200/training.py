@@ -1,9 +1,12 @@
 """What a training step runs around the head: the teacher-forced loss with its
 gradient, and the global gradient norm with clipping.
 
-A step is ``apply_block_logits`` -> ``block_cross_entropy`` ->
-``apply_block_logits_backward`` -> (the all-reduce of ``sharding``) ->
-``GradientClipper.clip``; ``VanillaMarkov.teacher_forced_gradients`` runs it.
+A step of one process is ``apply_block_logits`` -> ``block_cross_entropy`` ->
+``apply_block_logits_backward`` -> ``GradientClipper.clip``;
+``VanillaMarkov.teacher_forced_gradients`` runs it. With several ranks a program
+calls the parts: the all-reduce of ``sharding`` stands between the backward and
+the clipping, and a mean over all ranks takes ``reduction="sum"`` and a division
+by the sum of all ranks' weights.
 """
 from __future__ import annotations
 
@@ -90,8 +93,9 @@ class GradientClipper:
     overlap. ``out``: tensors of the same shapes and dtypes that take the
     clipped gradients (each its gradient itself or memory that overlaps none of
     them); None: in place. Creating the object lays the tensors out as a plan
-    in device memory (a host-to-device copy: create it before a graph capture);
-    ``clip`` reads what the tensors hold at each call. Calls of one object are
+    in device memory: a host-to-device copy for which the host waits, and with
+    it for the work before it on the stream. During a graph capture that is
+    refused; create the object before. ``clip`` reads what the tensors hold at each call. Calls of one object are
     ordered on one stream or by events, as anything that writes the same
     tensors is; the object is kept until they have run.
     """
@@ -110,6 +114,8 @@ class GradientClipper:
             _check_cuda(g, f"grads[{i}]", self.device)
             if o is not g:
                 _check_cuda(o, f"out[{i}]", self.device)
+        if grads and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("a GradientClipper is created before a graph capture, not during it")
         self.grads, self.outs = grads, outs
         self._starts = sorted((g.data_ptr(), i) for i, g in enumerate(grads) if g.numel())
         lib = N.load()
@@ -169,5 +175,7 @@ class GradientClipper:
 def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, *,
                    out: Optional[Sequence[torch.Tensor]] = None) -> torch.Tensor:
     """``GradientClipper(grads, out=out).clip(max_norm)`` for buffers that are
-    clipped once."""
+    clipped once. Making the object stops the host until the stream's work so
+    far has run, and is refused during a graph capture; buffers that are clipped
+    again and again want an object that is kept."""
     return GradientClipper(grads, out=out).clip(max_norm)

@@ -467,6 +467,25 @@ def test_clip_repeats_streams_and_graphs():
     _check_clip(norms[1], outs[1], fresh, 2.0)
 
 
+def test_clippers_are_not_made_during_a_capture():
+    """Refused before anything that would spoil the capture, which ends well; a clipper made before it is captured."""
+    g = torch.randn(5000, device="cuda")
+    want = g * 2
+    clipper = GradientClipper([g])
+    clipper.clip(math.inf)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for f in (lambda: GradientClipper([g]), lambda: clip_grad_norm([g], 1.0)):
+            with pytest.raises(RuntimeError):
+                f()
+        g.mul_(2)
+        norm = clipper.clip(math.inf)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(g, want) and abs(norm.item() - want.double().norm().item()) <= 1e-6 * norm.item()
+
+
 def test_clip_refusals():
     g = torch.zeros(100, device="cuda")
     for f in (lambda: GradientClipper([g.double()]), lambda: GradientClipper([g.cpu()]),
