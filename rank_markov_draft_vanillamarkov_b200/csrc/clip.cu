@@ -10,8 +10,8 @@
 //
 // Bound by memory: two readings and a writing of 132 MB (two fp32 [129280, 128])
 // take 68 us, 5.8 TB/s counted so; what the second reading finds in L2 (126 MB)
-// saves little of it, since the writing displaces it. A plan of one to sixteen
-// pieces takes 8 us, of which most is the launch; two launches took 20.
+// saves little of it, since the writing displaces it. A plan of one to eight
+// pieces takes 8 us, of which most is the launch.
 //
 // Squares of four elements are summed in 32 bits and then in 64. A group whose
 // sum leaves the range in which that is exact to a few roundings (it overflows,
@@ -30,7 +30,10 @@ constexpr int kThreads = 256;
 constexpr int kCtasPerSm = 3;
 constexpr int kInFlight = 8;  // 16-byte vectors per thread
 constexpr int kSmallCtas = 8;
-constexpr int64_t kSmallPieces = 16;  // up to 1 MB in all
+// Plans of one cluster: a piece for each of its CTAs, 512 KB in all. Eight pieces
+// take 5.7 us from a graph and 7.8 as called from Python, 5.9 and 10.5 in two
+// launches; sixteen would take 8.8 and 10.3, in two launches 6.0 and 10.6.
+constexpr int64_t kSmallPieces = kSmallCtas;
 
 __device__ __forceinline__ double block_sum(double x, double* parts) {
 #pragma unroll
