@@ -674,11 +674,14 @@ ConstrainPlan plan_constrain(const ConstrainArgs& a) {
   const int64_t vocab = round_up(a.vocab, kBlock);
   // Stretches: as many CTAs as run at once, and as few waves of them as the
   // largest stretch allows. Where there are few, rows go to different CTAs
-  // rather than one after another, each of which then reads the lists (7 x 5
-  // rows of 32003: 17 us, 30 with a sequence's rows in one CTA).
+  // rather than one after another, each of which then reads the lists, until
+  // stretches of 8192 ids fill the device. Kernels behind 1000 tokens with rows
+  // divided until stretches of 2048, 8192 and 32768 ids do: 16 x 8 rows of 32003
+  // ids 32.7, 17.0 and 16.9 us, 8 x 8 of 129280 46.7, 18.6 and 23.2, 32 x 8 of
+  // 129280 46.2, 46.2 and 50.9.
   const int64_t slots = kCopyCtas * num_sms;
   int64_t rows = a.block;
-  while (rows > 1 && a.batch * ((a.block + rows - 1) / rows) * (vocab / 2048 + 1) <= slots) rows = (rows + 1) / 2;
+  while (rows > 1 && a.batch * ((a.block + rows - 1) / rows) * (vocab / 8192 + 1) <= slots) rows = (rows + 1) / 2;
   p.rows = (int)std::min<int64_t>(rows, 0x7fffffff);
   p.groups = (int)((a.block + rows - 1) / rows);
   int64_t stretch = vocab;
