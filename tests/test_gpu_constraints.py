@@ -10,7 +10,7 @@ import torch
 from oracle import around
 from oracle.philox import gumbel_noise
 from rank_markov_draft_vanillamarkov_b200 import (DSparkError, TokenConstraints, VanillaMarkov, device_status,
-                                                  launch_count, process_logits, set_algo)
+                                                  last_algo, launch_count, process_logits, set_algo)
 from rank_markov_draft_vanillamarkov_b200 import _native as N
 from rank_markov_draft_vanillamarkov_b200.build import build
 
@@ -623,6 +623,21 @@ def test_constrained_sampler_of_rows_that_allow_nothing(vocab, dtype, temperatur
     assert torch.equal(tokens.cpu(), want)
     assert np.array_equal(f64(logits) > -np.inf, masks)
     assert device_status() == 0
+
+
+@pytest.mark.parametrize("batch,m,vocab,rank,ldt", [(3, 3, 129280, 128, torch.bfloat16),
+                                                    (2, 2, 129280, 64, torch.float32),
+                                                    (2, 4, 151936, 64, torch.bfloat16)])
+@pytest.mark.parametrize("temperature", [0.0, 0.8])
+def test_constrained_sampler_at_full_vocabularies(batch, m, vocab, rank, ldt, temperature):
+    """The strided corrections on the tensor cores, and lists in several parts of the vocabulary."""
+    test_constrained_sampler(batch, m, vocab, rank, ldt, torch.bfloat16, temperature)
+    assert last_algo() == 1  # process_logits came last
+    head = _head(vocab, rank, torch.bfloat16, seed=1)
+    head.sample_block_tokens(torch.zeros(batch, m, vocab, dtype=ldt, device="cuda"),
+                             first_prev_token_ids=torch.zeros(batch, dtype=torch.int64, device="cuda"),
+                             temperature=temperature, constraints=TokenConstraints(vocab))
+    assert last_algo() == 2
 
 
 def test_sampler_without_effective_constraints_is_the_plain_sampler():
