@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) copy_kernel(Constrain
   auto score = [&](float y, int64_t k, int l) {
     const uint32_t v = (uint32_t)(c0 + l);
     float q = y / a.temperature;
-    if (fabsf(q) >= 0x1p127f && !isinf(y)) q = copysignf(0x1p127f, y) + 0.25f * y;
+    if (fabsf(q) >= 0x1p127f) q = fmaf(0.25f, y, copysignf(0x1p127f, y));
     return pack_key(q + noise_for(a.seed, (uint32_t)b, (uint32_t)(a.draft_first + k), v), v);
   };
   const T* const in0 = static_cast<const T*>(a.in) + b * a.in_batch + c0;
