@@ -8,10 +8,12 @@
 // each CTA its own pieces again, the last first, since they were read last.
 // Small plans run both passes in one cluster, with its barrier between them.
 //
-// Bound by memory: two readings and a writing of 132 MB (two fp32 [129280, 128])
-// take 68 us, 5.8 TB/s counted so; what the second reading finds in L2 (126 MB)
-// saves little of it, since the writing displaces it. A plan of one to eight
-// pieces takes 8 us, of which most is the launch.
+// Two readings and a writing of 132 MB (two fp32 [129280, 128]) take 68 us, 5.8
+// TB/s counted so and bound by memory: of the second reading 79 MB come from
+// DRAM, the rest is still in L2 (126 MB). 55 MB in 182 tensors of both types
+// take 34.5 us: the second reading finds all of it in L2, but pieces in turn
+// give the fullest CTA 1.58 times the mean bytes (1.10 in the larger case). A
+// plan of one to eight pieces takes 8 us, of which most is the launch.
 //
 // Squares of four elements are summed in 32 bits and then in 64. A group whose
 // sum leaves the range in which that is exact to a few roundings (it overflows,

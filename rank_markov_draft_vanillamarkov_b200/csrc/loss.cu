@@ -21,10 +21,11 @@
 //
 // Measured: 2560 rows of 129280 bf16, a fifth of them ignored, 248 us (4.8 TB/s
 // of 1.19 GB; a plain copy of as many bytes 190 us), 320 rows 46 us (3.6 TB/s;
-// the copy 33 us), 320 fp32 rows 70 us (4.8 TB/s; 57 us). What keeps it from the
-// copy: two exponentials a logit at 16 per clock and SM take 18 us for 320 rows,
-// and 71 clusters of four run at once, so that 320 rows go in five rounds of
-// which the last is half empty.
+// the copy 33 us), 320 fp32 rows 70.5 us (4.7 TB/s; 57 us). What keeps it from the
+// copy: two exponentials a logit at 16 per clock and SM are 18 us for 320 rows
+// (the pipe that makes them is busy for 24 of a launch's 43), and 71 clusters of
+// four run at once, so that 320 rows go in five rounds of which the last is half
+// empty. Without the gradient 320 rows take 32 us.
 #include <algorithm>
 #include <cmath>
 #include <mutex>
@@ -501,7 +502,9 @@ __global__ void __launch_bounds__(kMaxThreads, 2) loss_rows_kernel(LossArgs a, L
   }
 }
 
-// Rows longer than a cluster's registers: one CTA per row reads it twice.
+// Rows longer than a cluster's registers (524288 bf16 or 262144 fp32 ids): one
+// CTA per row reads it twice, an element at a time. 64 rows of 600001 bf16 ids
+// take 863 us, 132 without the gradient; their traffic is worth 35.
 template <typename T>
 __global__ void __launch_bounds__(kSumThreads) loss_long_rows_kernel(LossArgs a) {
   __shared__ double sums[kSumThreads / 32];
