@@ -114,7 +114,7 @@ class GradientClipper:
             _check_cuda(g, f"grads[{i}]", self.device)
             if o is not g:
                 _check_cuda(o, f"out[{i}]", self.device)
-        if grads and torch.cuda.is_current_stream_capturing():
+        if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("a GradientClipper is created before a graph capture, not during it")
         self.grads, self.outs = grads, outs
         self._starts = sorted((g.data_ptr(), i) for i, g in enumerate(grads) if g.numel())

@@ -476,7 +476,7 @@ def test_clippers_are_not_made_during_a_capture():
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        for f in (lambda: GradientClipper([g]), lambda: clip_grad_norm([g], 1.0)):
+        for f in (lambda: GradientClipper([g]), lambda: clip_grad_norm([g], 1.0), lambda: clip_grad_norm([], 1.0)):
             with pytest.raises(RuntimeError):
                 f()
         g.mul_(2)
